@@ -2,12 +2,15 @@
 // Every check runs before any HIP call, so invalid arguments are rejected
 // identically on machines without a GPU.
 #include <algorithm>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
 #include <mutex>
 
 #include "common.h"
+#include "kvcache.h"
+#include "rope.h"
 
 #ifndef GNF4_REVISION
 #define GNF4_REVISION "unknown"
@@ -611,6 +614,311 @@ gnf4_status gnf4_expert_cache_fill(const gnf4_weights *host_w, const gnf4_weight
   f.S = cache_w->E;
   f.copies = copies;
   return device_status(launch_cache_fill(f, max_copies, (hipStream_t)stream), "cache fill launch");
+}
+
+// ------------------------------------------------ attention
+
+// q or k of the head norm + rotation: H heads of D values per token.
+static gnf4_status check_heads(const char *name, const void *p, int64_t stride, int32_t H, int32_t D) {
+  if (H == 0) return ok();
+  if (!p) return fail(GNF4_ERR_INVALID_ARG, "%s is NULL", name);
+  if (!aligned16(p)) return fail(GNF4_ERR_INVALID_ARG, "%s must be 16-byte aligned", name);
+  if (stride % 8 || stride < (int64_t)H * D)
+    return fail(GNF4_ERR_INVALID_ARG, "the stride %lld of %s must be a multiple of 8 and at least %lld",
+                (long long)stride, name, (long long)H * D);
+  return ok();
+}
+
+static gnf4_status check_norm_rope(int32_t T, int32_t Hq, int32_t Hk, int32_t D, const void *wq, const void *wk,
+                                   float eps, const gnf4_rope *rope, const int32_t *positions) {
+  if (T < 0) return fail(GNF4_ERR_INVALID_ARG, "T = %d is negative", T);
+  if (Hq < 0 || Hk < 0 || Hq + (int64_t)Hk < 1 || Hq + (int64_t)Hk > 65535)
+    return fail(GNF4_ERR_INVALID_ARG, "Hq = %d and Hk = %d must give 1 to 65535 heads", Hq, Hk);
+  if (D < 16 || D > 256 || D % 8)
+    return fail(GNF4_ERR_INVALID_ARG, "D = %d must be a multiple of 8 in [16, 256]", D);
+  if (!(eps >= 0.0f) || std::isinf(eps)) return fail(GNF4_ERR_INVALID_ARG, "eps must be finite and not negative");
+  if (!aligned16(wq) || !aligned16(wk)) return fail(GNF4_ERR_INVALID_ARG, "wq and wk must be 16-byte aligned");
+  if (rope) {
+    if (rope->rot_dim < 16 || rope->rot_dim % 16 || rope->rot_dim > D)
+      return fail(GNF4_ERR_INVALID_ARG, "rot_dim = %d must be a multiple of 16 up to D = %d", rope->rot_dim, D);
+    if (rope->interleaved != 0 && rope->interleaved != 1)
+      return fail(GNF4_ERR_INVALID_ARG, "interleaved must be 0 or 1");
+    if (!rope->inv_freq || ((uintptr_t)rope->inv_freq & 3u))
+      return fail(GNF4_ERR_INVALID_ARG, "inv_freq must be a 4-byte aligned device pointer");
+    if (T > 0 && !positions) return fail(GNF4_ERR_INVALID_ARG, "positions is NULL");
+  }
+  return ok();
+}
+
+static RopeArgs rope_args(int32_t T, int32_t Hq, int32_t Hk, int32_t D, const uint16_t *wq, const uint16_t *wk,
+                          float eps, const gnf4_rope *rope, const int32_t *positions) {
+  RopeArgs a{};
+  a.T = T;
+  a.Hq = Hq;
+  a.Hk = Hk;
+  a.D = D;
+  a.wq = wq;
+  a.wk = wk;
+  a.eps = eps;
+  if (rope) {
+    a.rot = rope->rot_dim;
+    a.interleaved = rope->interleaved;
+    a.inv_freq = rope->inv_freq;
+    a.mscale = rope->mscale;
+    a.positions = positions;
+  }
+  return a;
+}
+
+gnf4_status gnf4_rope_frequencies(int32_t rot_dim, double base, int32_t scaling, double factor, double original_len,
+                                  double beta_fast, double beta_slow, float *inv_freq, float *mscale) {
+  if (rot_dim < 2 || rot_dim % 2 || rot_dim > 256)
+    return fail(GNF4_ERR_INVALID_ARG, "rot_dim = %d must be a multiple of 2 in [2, 256]", rot_dim);
+  if (!(base > 1.0) || std::isinf(base)) return fail(GNF4_ERR_INVALID_ARG, "base must be above 1");
+  if (scaling < GNF4_ROPE_PLAIN || scaling > GNF4_ROPE_YARN)
+    return fail(GNF4_ERR_INVALID_ARG, "unknown rotation scaling %d", scaling);
+  if (scaling != GNF4_ROPE_PLAIN && (!(factor >= 1.0) || std::isinf(factor)))
+    return fail(GNF4_ERR_INVALID_ARG, "factor must be at least 1");
+  if (scaling == GNF4_ROPE_YARN && (!(original_len > 0.0) || !(beta_slow >= 0.0) || !(beta_fast > beta_slow)))
+    return fail(GNF4_ERR_INVALID_ARG, "YARN needs original_len > 0 and 0 <= beta_slow < beta_fast");
+  if (!inv_freq) return fail(GNF4_ERR_INVALID_ARG, "inv_freq is NULL");
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    double f = std::pow(base, -2.0 * i / rot_dim);
+    if (scaling == GNF4_ROPE_LINEAR) f /= factor;
+    if (scaling == GNF4_ROPE_YARN) {
+      const double r = original_len * f / 6.283185307179586476925;
+      const double g = std::min(std::max((r - beta_slow) / (beta_fast - beta_slow), 0.0), 1.0);
+      f *= g + (1.0 - g) / factor;
+    }
+    inv_freq[i] = (float)f;
+  }
+  if (mscale) *mscale = scaling == GNF4_ROPE_YARN ? (float)(0.1 * std::log(factor) + 1.0) : 1.0f;
+  return ok();
+}
+
+gnf4_status gnf4_qk_norm_rope(const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t k_stride, int32_t T,
+                              int32_t Hq, int32_t Hk, int32_t D, const uint16_t *wq, const uint16_t *wk, float eps,
+                              const gnf4_rope *rope, const int32_t *positions, uint16_t *q_out, int64_t q_out_stride,
+                              uint16_t *k_out, int64_t k_out_stride, gnf4_stream_t stream) {
+  gnf4_status st = check_norm_rope(T, Hq, Hk, D, wq, wk, eps, rope, positions);
+  if (st != GNF4_OK) return st;
+  if (T == 0) return ok();
+  if ((st = check_heads("q", q, q_stride, Hq, D)) != GNF4_OK) return st;
+  if ((st = check_heads("k", k, k_stride, Hk, D)) != GNF4_OK) return st;
+  if ((st = check_heads("q_out", q_out, q_out_stride, Hq, D)) != GNF4_OK) return st;
+  if ((st = check_heads("k_out", k_out, k_out_stride, Hk, D)) != GNF4_OK) return st;
+  RopeArgs a = rope_args(T, Hq, Hk, D, wq, wk, eps, rope, positions);
+  a.q = q;
+  a.q_stride = q_stride;
+  a.k = k;
+  a.k_stride = k_stride;
+  a.q_out = q_out;
+  a.q_out_stride = q_out_stride;
+  a.k_out = k_out;
+  a.k_out_stride = k_out_stride;
+  return device_status(launch_norm_rope(a, (hipStream_t)stream), "head norm + rotation launch");
+}
+
+size_t gnf4_qk_norm_rope_dx_workspace_bytes(int32_t T, int32_t D) {
+  if (T < 0 || D < 16 || D > 256 || D % 8) return 0;
+  return (size_t)std::max(rope_dx_blocks(T), 1) * 2 * D * 4;
+}
+
+gnf4_status gnf4_qk_norm_rope_dx(const uint16_t *dq, int64_t dq_stride, const uint16_t *dk, int64_t dk_stride,
+                                 const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t k_stride, int32_t T,
+                                 int32_t Hq, int32_t Hk, int32_t D, const uint16_t *wq, const uint16_t *wk, float eps,
+                                 const gnf4_rope *rope, const int32_t *positions, uint16_t *gq, int64_t gq_stride,
+                                 uint16_t *gk, int64_t gk_stride, float *dwq, float *dwk, void *workspace,
+                                 size_t workspace_bytes, gnf4_stream_t stream) {
+  gnf4_status st = check_norm_rope(T, Hq, Hk, D, wq, wk, eps, rope, positions);
+  if (st != GNF4_OK) return st;
+  if ((dwq && !wq) || (dwk && !wk))
+    return fail(GNF4_ERR_INVALID_ARG, "a weight gradient is asked for a norm without a weight");
+  if (((uintptr_t)dwq | (uintptr_t)dwk) & 3u)
+    return fail(GNF4_ERR_INVALID_ARG, "dwq and dwk must be 4-byte aligned");
+  if (T > 0) {
+    if ((st = check_heads("dq", dq, dq_stride, Hq, D)) != GNF4_OK) return st;
+    if ((st = check_heads("dk", dk, dk_stride, Hk, D)) != GNF4_OK) return st;
+    if (wq && (st = check_heads("q", q, q_stride, Hq, D)) != GNF4_OK) return st;
+    if (wk && (st = check_heads("k", k, k_stride, Hk, D)) != GNF4_OK) return st;
+    if ((st = check_heads("gq", gq, gq_stride, Hq, D)) != GNF4_OK) return st;
+    if ((st = check_heads("gk", gk, gk_stride, Hk, D)) != GNF4_OK) return st;
+  }
+  RopeArgs a = rope_args(T, Hq, Hk, D, wq, wk, eps, rope, positions);
+  if (dwq || dwk) {
+    const size_t need = gnf4_qk_norm_rope_dx_workspace_bytes(T, D);
+    if (workspace_bytes < need)
+      return fail(GNF4_ERR_WORKSPACE, "workspace of %zu bytes given, %zu needed for T = %d, D = %d", workspace_bytes,
+                  need, T, D);
+    if (!workspace || !aligned16(workspace))
+      return fail(GNF4_ERR_INVALID_ARG, "workspace must be a 16-byte aligned device pointer");
+    a.part = (float *)workspace;
+    a.dwq = dwq;
+    a.dwk = dwk;
+  } else if (T == 0) {
+    return ok();
+  }
+  a.dq = dq;
+  a.dq_stride = dq_stride;
+  a.dk = dk;
+  a.dk_stride = dk_stride;
+  a.q = q;
+  a.q_stride = q_stride;
+  a.k = k;
+  a.k_stride = k_stride;
+  a.q_out = gq;
+  a.q_out_stride = gq_stride;
+  a.k_out = gk;
+  a.k_out_stride = gk_stride;
+  return device_status(launch_norm_rope_dx(a, (hipStream_t)stream), "head norm + rotation backward launch");
+}
+
+static gnf4_status check_kv_sizes(const gnf4_kv_cache *c, const gnf4_kv_batch *b) {
+  if (!c || !b) return fail(GNF4_ERR_INVALID_ARG, "cache or batch descriptor is NULL");
+  if (c->format == GNF4_NF4_DQ)
+    return fail(GNF4_ERR_UNSUPPORTED, "a cache in NF4_DQ: its second-level scales span rows written apart");
+  if (c->format != GNF4_NF4 && c->format != GNF4_MXFP4)
+    return fail(GNF4_ERR_INVALID_ARG, "unknown format %d", c->format);
+  if (c->n_pages < 1) return fail(GNF4_ERR_INVALID_ARG, "n_pages = %d must be positive", c->n_pages);
+  if (c->page_size < 16 || c->page_size > 65536 || (c->page_size & (c->page_size - 1)))
+    return fail(GNF4_ERR_INVALID_ARG, "page_size = %d must be a power of two in [16, 65536]", c->page_size);
+  if (c->H < 1 || c->H > 1024) return fail(GNF4_ERR_INVALID_ARG, "H = %d outside [1, 1024]", c->H);
+  if (c->D != 64 && c->D != 128 && c->D != 256)
+    return fail(GNF4_ERR_UNSUPPORTED, "D = %d must be 64, 128 or 256", c->D);
+  if (b->B < 0 || b->B > 1 << 20) return fail(GNF4_ERR_INVALID_ARG, "B = %d outside [0, 2^20]", b->B);
+  if (b->n_tokens < 0) return fail(GNF4_ERR_INVALID_ARG, "n_tokens = %d is negative", b->n_tokens);
+  if (b->max_new < 1 && b->n_tokens > 0 && b->B > 0)
+    return fail(GNF4_ERR_INVALID_ARG, "max_new = %d must be positive", b->max_new);
+  if (b->max_pages < 1 || (int64_t)b->max_pages * c->page_size > (int64_t)1 << 30)
+    return fail(GNF4_ERR_INVALID_ARG, "max_pages = %d must be positive, max_pages * page_size at most 2^30",
+                b->max_pages);
+  if ((int64_t)b->n_tokens * c->H * (c->D / 4) > 0x7fffffffLL * 256)
+    return fail(GNF4_ERR_UNSUPPORTED, "too many rows for one call");
+  return ok();
+}
+
+static gnf4_status check_kv(const gnf4_kv_cache *c, const gnf4_kv_batch *b) {
+  gnf4_status st = check_kv_sizes(c, b);
+  if (st != GNF4_OK) return st;
+  if (!c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales)
+    return fail(GNF4_ERR_INVALID_ARG, "a cache array is NULL");
+  if (!aligned16(c->k_codes) || !aligned16(c->k_scales) || !aligned16(c->v_codes) || !aligned16(c->v_scales))
+    return fail(GNF4_ERR_INVALID_ARG, "the cache arrays must be 16-byte aligned");
+  if (b->n_tokens > 0 && b->B > 0) {
+    if (!b->offsets || !b->lens || !b->pages) return fail(GNF4_ERR_INVALID_ARG, "offsets, lens or pages is NULL");
+    if (((uintptr_t)b->offsets | (uintptr_t)b->lens | (uintptr_t)b->pages) & 3u)
+      return fail(GNF4_ERR_INVALID_ARG, "offsets, lens and pages must be 4-byte aligned");
+  }
+  return ok();
+}
+
+static KvView kv_view(const gnf4_kv_cache *c, const gnf4_kv_batch *b) {
+  KvView v{};
+  v.k_codes = c->k_codes;
+  v.v_codes = c->v_codes;
+  v.k_scales = c->k_scales;
+  v.v_scales = c->v_scales;
+  v.n_pages = c->n_pages;
+  v.page_shift = __builtin_ctz((unsigned)c->page_size);
+  v.H = c->H;
+  v.D = c->D;
+  v.offsets = b->offsets;
+  v.lens = b->lens;
+  v.pages = b->pages;
+  v.B = b->B;
+  v.n_tokens = b->n_tokens;
+  v.max_pages = b->max_pages;
+  return v;
+}
+
+gnf4_status gnf4_kv_cache_write(const gnf4_kv_cache *cache, const gnf4_kv_batch *batch, const uint16_t *k,
+                                int64_t k_stride, const uint16_t *v, int64_t v_stride, gnf4_stream_t stream) {
+  gnf4_status st = check_kv(cache, batch);
+  if (st != GNF4_OK) return st;
+  if (batch->n_tokens == 0 || batch->B == 0) return ok();
+  if ((st = check_heads("k", k, k_stride, cache->H, cache->D)) != GNF4_OK) return st;
+  if ((st = check_heads("v", v, v_stride, cache->H, cache->D)) != GNF4_OK) return st;
+  KvRowsArgs a{};
+  a.kv = kv_view(cache, batch);
+  a.k = k;
+  a.k_stride = k_stride;
+  a.v = v;
+  a.v_stride = v_stride;
+  return device_status(launch_kv_write(a, cache->format, (hipStream_t)stream), "cache write launch");
+}
+
+gnf4_status gnf4_kv_cache_read(const gnf4_kv_cache *cache, const gnf4_kv_batch *batch, int32_t out_f32, void *k,
+                               void *v, gnf4_stream_t stream) {
+  gnf4_status st = check_kv(cache, batch);
+  if (st != GNF4_OK) return st;
+  if (out_f32 != 0 && out_f32 != 1) return fail(GNF4_ERR_INVALID_ARG, "out_f32 must be 0 or 1");
+  if (batch->n_tokens == 0 || batch->B == 0) return ok();
+  if (!k || !v) return fail(GNF4_ERR_INVALID_ARG, "k or v is NULL");
+  if (!aligned16(k) || !aligned16(v)) return fail(GNF4_ERR_INVALID_ARG, "k and v must be 16-byte aligned");
+  KvRowsArgs a{};
+  a.kv = kv_view(cache, batch);
+  a.k_out = k;
+  a.v_out = v;
+  return device_status(launch_kv_read(a, cache->format, out_f32, (hipStream_t)stream), "cache read launch");
+}
+
+// The plan of an attention call whose sizes have been checked.
+static gnf4_status attention_plan(const gnf4_kv_cache *c, const gnf4_kv_batch *b, int32_t Hq, int32_t window,
+                                  KvAttnPlan *p) {
+  if (Hq < 1 || Hq > 65536 || Hq % c->H)
+    return fail(GNF4_ERR_INVALID_ARG, "Hq = %d must be a multiple of H = %d up to 65536", Hq, c->H);
+  if (window < 0) return fail(GNF4_ERR_INVALID_ARG, "window = %d is negative", window);
+  const int32_t most = std::min(b->max_new, b->n_tokens);
+  const int64_t len = std::min<int64_t>(std::max(b->max_len, 1), (int64_t)b->max_pages * c->page_size);
+  if ((int64_t)b->n_tokens * (Hq / c->H) > 0x3fffffffLL ||
+      !kv_attention_plan(c->D, c->H, Hq / c->H, b->B, b->n_tokens, most, len, window, p))
+    return fail(GNF4_ERR_UNSUPPORTED, "too many rows for one call");
+  return ok();
+}
+
+size_t gnf4_kv_attention_workspace_bytes(const gnf4_kv_cache *cache, const gnf4_kv_batch *batch, int32_t Hq,
+                                         int32_t window) {
+  KvAttnPlan p;
+  if (check_kv_sizes(cache, batch) != GNF4_OK || batch->n_tokens == 0 || batch->B == 0 ||
+      attention_plan(cache, batch, Hq, window, &p) != GNF4_OK)
+    return 0;
+  return p.bytes;
+}
+
+gnf4_status gnf4_kv_attention(const uint16_t *q, int64_t q_stride, const gnf4_kv_cache *cache,
+                              const gnf4_kv_batch *batch, int32_t Hq, float scale, int32_t window, const float *sinks,
+                              uint16_t *out, int64_t out_stride, float *lse, void *workspace, size_t workspace_bytes,
+                              gnf4_stream_t stream) {
+  gnf4_status st = check_kv(cache, batch);
+  if (st != GNF4_OK) return st;
+  if (!std::isfinite(scale)) return fail(GNF4_ERR_INVALID_ARG, "scale must be finite");
+  KvAttnPlan p{};
+  const bool empty = batch->n_tokens == 0 || batch->B == 0;
+  gnf4_kv_batch one = *batch;
+  if (empty) one.B = one.n_tokens = one.max_new = 1;         // the other checks as ever
+  if ((st = attention_plan(cache, &one, Hq, window, &p)) != GNF4_OK) return st;
+  if (empty) return ok();
+  if ((st = check_heads("q", q, q_stride, Hq, cache->D)) != GNF4_OK) return st;
+  if ((st = check_heads("out", out, out_stride, Hq, cache->D)) != GNF4_OK) return st;
+  if (((uintptr_t)sinks | (uintptr_t)lse) & 3u)
+    return fail(GNF4_ERR_INVALID_ARG, "sinks and lse must be 4-byte aligned");
+  if (workspace_bytes < p.bytes)
+    return fail(GNF4_ERR_WORKSPACE, "attention workspace of %zu bytes given, %zu needed", workspace_bytes, p.bytes);
+  if (p.bytes && (!workspace || !aligned16(workspace)))
+    return fail(GNF4_ERR_INVALID_ARG, "workspace must be a 16-byte aligned device pointer");
+  KvAttnArgs a{};
+  a.kv = kv_view(cache, batch);
+  a.q = q;
+  a.q_stride = q_stride;
+  a.out = out;
+  a.out_stride = out_stride;
+  a.lse = lse;
+  a.sinks = sinks;
+  a.G = Hq / cache->H;
+  a.window = window;
+  a.scale_log2 = (float)((double)scale * 1.4426950408889634074);
+  a.part = (float *)workspace;
+  return device_status(launch_kv_attention(a, p, cache->format, (hipStream_t)stream), "attention launch");
 }
 
 void gnf4_nf4_codebook(float out[16]) {

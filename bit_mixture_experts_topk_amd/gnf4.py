@@ -32,6 +32,9 @@ EXPORTS = ("gnf4_route", "gnf4_route_workspace_bytes", "gnf4_route_noalloc", "gn
            "gnf4_nf4_codebook_bf16", "gnf4_read_probe",
            "gnf4_expert_cache_state_words", "gnf4_expert_cache_copies_words",
            "gnf4_expert_cache_reset", "gnf4_expert_cache_stage", "gnf4_expert_cache_fill",
+           "gnf4_rope_frequencies", "gnf4_qk_norm_rope", "gnf4_qk_norm_rope_dx",
+           "gnf4_qk_norm_rope_dx_workspace_bytes", "gnf4_kv_cache_write", "gnf4_kv_cache_read",
+           "gnf4_kv_attention", "gnf4_kv_attention_workspace_bytes",
            "gnf4_last_error",
            "gnf4_build_id")
 
@@ -46,6 +49,23 @@ class CWeights(ctypes.Structure):
     _fields_ = [("format", ctypes.c_int32), ("E", ctypes.c_int32), ("N", ctypes.c_int32),
                 ("K", ctypes.c_int32), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
                 ("scales2", ctypes.c_void_p)]
+
+
+class CRope(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("inv_freq", ctypes.c_void_p), ("mscale", ctypes.c_float)]
+
+
+class CKVCache(ctypes.Structure):
+    _fields_ = [("format", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("H", ctypes.c_int32), ("D", ctypes.c_int32), ("k_codes", ctypes.c_void_p),
+                ("k_scales", ctypes.c_void_p), ("v_codes", ctypes.c_void_p), ("v_scales", ctypes.c_void_p)]
+
+
+class CKVBatch(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("n_tokens", ctypes.c_int32), ("max_new", ctypes.c_int32),
+                ("max_len", ctypes.c_int32), ("offsets", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("pages", ctypes.c_void_p), ("max_pages", ctypes.c_int32)]
 
 
 _lib = None
@@ -86,6 +106,19 @@ def lib():
         L.gnf4_expert_cache_reset.argtypes = [P, I, I, S]
         L.gnf4_expert_cache_stage.argtypes = [P, I, I, I, I, P, P, P, S]
         L.gnf4_expert_cache_fill.argtypes = [ctypes.POINTER(CWeights), ctypes.POINTER(CWeights), P, I, S]
+        F, W, RP = ctypes.c_float, ctypes.c_int64, ctypes.POINTER(CRope)
+        D, CP, BP = ctypes.c_double, ctypes.POINTER(CKVCache), ctypes.POINTER(CKVBatch)
+        L.gnf4_rope_frequencies.argtypes = [I, D, I, D, D, D, D, ctypes.POINTER(F), ctypes.POINTER(F)]
+        L.gnf4_qk_norm_rope.argtypes = [P, W, P, W, I, I, I, I, P, P, F, RP, P, P, W, P, W, S]
+        L.gnf4_qk_norm_rope_dx.argtypes = [P, W, P, W, P, W, P, W, I, I, I, I, P, P, F, RP, P, P, W, P, W,
+                                           P, P, P, Z, S]
+        L.gnf4_qk_norm_rope_dx_workspace_bytes.argtypes = [I, I]
+        L.gnf4_qk_norm_rope_dx_workspace_bytes.restype = Z
+        L.gnf4_kv_cache_write.argtypes = [CP, BP, P, W, P, W, S]
+        L.gnf4_kv_cache_read.argtypes = [CP, BP, I, P, P, S]
+        L.gnf4_kv_attention.argtypes = [P, W, CP, BP, I, F, I, P, P, W, P, P, Z, S]
+        L.gnf4_kv_attention_workspace_bytes.argtypes = [CP, BP, I, I]
+        L.gnf4_kv_attention_workspace_bytes.restype = Z
         L.gnf4_nf4_codebook.argtypes = [ctypes.POINTER(ctypes.c_float)]
         L.gnf4_nf4_codebook.restype = None
         L.gnf4_nf4_codebook_bf16.argtypes = [ctypes.POINTER(ctypes.c_uint16), ctypes.POINTER(ctypes.c_float)]
@@ -502,3 +535,234 @@ def expert_cache_fill(host_w, cache_w, copies, max_copies):
     hw, cw = host_w.cstruct(), cache_w.cstruct()
     _check(lib().gnf4_expert_cache_fill(ctypes.byref(hw), ctypes.byref(cw), _ptr(copies), max_copies,
                                         _stream()), "gnf4_expert_cache_fill")
+
+
+# ------------------------------------------------ attention
+
+ROPE_SCALINGS = {"plain": 0, "linear": 1, "yarn": 2}
+
+
+@dataclass
+class Rope:
+    """Rotation by position: pair i of a head's first 2 * len(inv_freq) values
+    turns by position * inv_freq[i] (float32, CUDA); pairs are neighbours when
+    interleaved, else the two halves; both are multiplied by mscale."""
+    inv_freq: torch.Tensor
+    interleaved: bool = False
+    mscale: float = 1.0
+
+    def cstruct(self):
+        return CRope(2 * self.inv_freq.numel(), int(self.interleaved), self.inv_freq.data_ptr(), self.mscale)
+
+
+@dataclass
+class KVCache:
+    """A paged 4-bit cache of keys and values: codes uint8 [n_pages, H,
+    page_size, D/2], scales float32 [.., D/64] (NF4) or uint8 [.., D/32] (MXFP4)."""
+    format: int
+    n_pages: int
+    page_size: int
+    H: int
+    D: int
+    k_codes: torch.Tensor
+    k_scales: torch.Tensor
+    v_codes: torch.Tensor
+    v_scales: torch.Tensor
+
+    def cstruct(self):
+        codes, scales = (self.k_codes, self.v_codes), (self.k_scales, self.v_scales)
+        rows = self.n_pages * self.H * self.page_size
+        mx = self.format == MXFP4
+        for c, s in zip(codes, scales):
+            _here(c, torch.uint8, "cache codes")
+            _here(s, torch.uint8 if mx else torch.float32, "cache scales")
+            if c.numel() != rows * (self.D // 2) or s.numel() != rows * (self.D // (32 if mx else 64)):
+                raise ValueError("the cache arrays do not hold n_pages * H * page_size rows of D values")
+        return CKVCache(self.format, self.n_pages, self.page_size, self.H, self.D, codes[0].data_ptr(),
+                        scales[0].data_ptr(), codes[1].data_ptr(), scales[1].data_ptr())
+
+    def nbytes(self):
+        return sum(t.numel() * t.element_size() for t in (self.k_codes, self.k_scales, self.v_codes, self.v_scales))
+
+
+@dataclass
+class KVBatch:
+    """The rows of a step: sequence b's new tokens are rows [offsets[b],
+    offsets[b+1]), lens[b] its length with them, pages[b] its page ids (all
+    int32, CUDA). max_new bounds the new tokens of one sequence, max_len is
+    the longest length expected."""
+    offsets: torch.Tensor
+    lens: torch.Tensor
+    pages: torch.Tensor
+    n_tokens: int
+    max_new: int
+    max_len: int
+
+    def cstruct(self):
+        for name in ("offsets", "lens", "pages"):
+            _here(getattr(self, name), torch.int32, name)
+        B = self.lens.numel()
+        if self.offsets.numel() != B + 1 or self.pages.dim() != 2 or self.pages.shape[0] != B:
+            raise ValueError("offsets must hold B + 1, lens B and pages B rows of ids")
+        return CKVBatch(B, self.n_tokens, self.max_new, self.max_len, self.offsets.data_ptr(),
+                        self.lens.data_ptr(), self.pages.data_ptr(), self.pages.shape[1])
+
+
+def _here(t, dtype, name):
+    """t: a contiguous tensor of that type on the current device."""
+    if not (t.is_cuda and t.dtype == dtype and t.is_contiguous()):
+        raise ValueError("%s must be a contiguous %s CUDA tensor" % (name, dtype))
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError("%s lies on %s, which is not the current device" % (name, t.device))
+    return t
+
+
+def _heads(t, T, H, D, name):
+    """t: bf16 (or 16-bit pattern) [T, H, D] on the current device, any token stride."""
+    if not (t.is_cuda and t.element_size() == 2 and t.dim() == 3 and t.shape == (T, H, D)):
+        raise ValueError("%s must be a bf16 (or 16-bit bit pattern) CUDA tensor [%d, %d, %d]" % (name, T, H, D))
+    if t.dtype == torch.float16:
+        raise ValueError("%s is float16, not bf16" % name)
+    s = t.stride()
+    if t.numel() and (s[2] != 1 or (s[1] != D and H > 1)):
+        raise ValueError("the heads of %s must be contiguous within a token" % name)
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError("%s lies on %s, which is not the current device" % (name, t.device))
+    return t
+
+
+def _tstride(t):
+    """Token stride in elements (of a single token: its own size)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def rope_frequencies(rot_dim, base=10000.0, scaling="plain", factor=1.0, original_len=0.0, beta_fast=32.0,
+                     beta_slow=1.0, interleaved=False, device="cuda"):
+    """A Rope with the frequencies of gnf4_rope_frequencies on the device."""
+    f, m = (ctypes.c_float * max(rot_dim // 2, 1))(), ctypes.c_float()
+    _check(lib().gnf4_rope_frequencies(rot_dim, base, ROPE_SCALINGS.get(scaling, scaling), factor, original_len,
+                                       beta_fast, beta_slow, f, ctypes.byref(m)), "gnf4_rope_frequencies")
+    return Rope(torch.tensor(list(f), dtype=torch.float32, device=device), interleaved, m.value)
+
+
+def _rope_call(positions, rope, T, wq, wk, D):
+    if rope is not None:
+        _here(rope.inv_freq, torch.float32, "inv_freq")
+        _here(positions, torch.int32, "positions")
+        if positions.numel() != T:
+            raise ValueError("positions must hold T = %d values" % T)
+    for w, name in ((wq, "wq"), (wk, "wk")):
+        if w is not None and (w.numel() != D or w.element_size() != 2 or w.dtype == torch.float16):
+            raise ValueError("%s must hold D = %d bf16 values" % (name, D))
+        if w is not None:
+            _here(w, w.dtype, name)
+    return None if rope is None else ctypes.byref(rope.cstruct())
+
+
+def qk_norm_rope(q, k, positions, rope=None, wq=None, wk=None, eps=1e-6, q_out=None, k_out=None):
+    """Norm (bf16 weights wq, wk [D]; None: no norm) and rotation (None: none)
+    of q [T, Hq, D] and k [T, Hk, D] (bf16, any token stride) at int32
+    positions [T]; returns (q_out, k_out), which may be q and k themselves."""
+    T, Hq, D = q.shape
+    Hk = k.shape[1]
+    _heads(q, T, Hq, D, "q")
+    _heads(k, T, Hk, D, "k")
+    r = _rope_call(positions, rope, T, wq, wk, D)
+    q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device) if q_out is None else _heads(q_out, T, Hq, D, "q_out")
+    k_out = torch.empty((T, Hk, D), dtype=k.dtype, device=k.device) if k_out is None else _heads(k_out, T, Hk, D, "k_out")
+    _check(lib().gnf4_qk_norm_rope(q.data_ptr(), _tstride(q), k.data_ptr(), _tstride(k), T, Hq, Hk, D, _ptr(wq), _ptr(wk),
+                                   eps, r, _ptr(positions), q_out.data_ptr(), _tstride(q_out), k_out.data_ptr(),
+                                   _tstride(k_out), _stream()), "gnf4_qk_norm_rope")
+    return q_out, k_out
+
+
+def qk_norm_rope_dx(dq, dk, q, k, positions, rope=None, wq=None, wk=None, eps=1e-6, gq=None, gk=None,
+                    workspace=None):
+    """Backward pass of qk_norm_rope: (gq, gk, dwq, dwk) from the gradients dq,
+    dk of its results and its inputs; dwq / dwk float32 [D], None without a
+    weight. gq and gk may be dq and dk."""
+    T, Hq, D = dq.shape
+    Hk = dk.shape[1]
+    _heads(dq, T, Hq, D, "dq")
+    _heads(dk, T, Hk, D, "dk")
+    _heads(q, T, Hq, D, "q")
+    _heads(k, T, Hk, D, "k")
+    r = _rope_call(positions, rope, T, wq, wk, D)
+    gq = torch.empty((T, Hq, D), dtype=dq.dtype, device=dq.device) if gq is None else _heads(gq, T, Hq, D, "gq")
+    gk = torch.empty((T, Hk, D), dtype=dk.dtype, device=dk.device) if gk is None else _heads(gk, T, Hk, D, "gk")
+    dwq = torch.empty(D, dtype=torch.float32, device=dq.device) if wq is not None else None
+    dwk = torch.empty(D, dtype=torch.float32, device=dq.device) if wk is not None else None
+    if workspace is None and (wq is not None or wk is not None):
+        workspace = torch.empty(lib().gnf4_qk_norm_rope_dx_workspace_bytes(T, D), dtype=torch.uint8, device=dq.device)
+    _check(lib().gnf4_qk_norm_rope_dx(dq.data_ptr(), _tstride(dq), dk.data_ptr(), _tstride(dk), q.data_ptr(), _tstride(q),
+                                      k.data_ptr(), _tstride(k), T, Hq, Hk, D, _ptr(wq), _ptr(wk), eps, r,
+                                      _ptr(positions), gq.data_ptr(), _tstride(gq), gk.data_ptr(), _tstride(gk),
+                                      _ptr(dwq), _ptr(dwk), _ptr(workspace),
+                                      0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                      _stream()), "gnf4_qk_norm_rope_dx")
+    return gq, gk, dwq, dwk
+
+
+def empty_kv_cache(fmt, n_pages, page_size, H, D, device="cuda"):
+    """An uninitialised cache of n_pages pages of page_size positions."""
+    fmt = FORMATS.get(fmt, fmt)
+    codes = [torch.empty((n_pages, H, page_size, D // 2), dtype=torch.uint8, device=device) for _ in range(2)]
+    mx = fmt == MXFP4
+    scales = [torch.empty((n_pages, H, page_size, D // (32 if mx else 64)),
+                          dtype=torch.uint8 if mx else torch.float32, device=device) for _ in range(2)]
+    return KVCache(fmt, n_pages, page_size, H, D, codes[0], scales[0], codes[1], scales[1])
+
+
+def kv_cache_write(cache, k, v, batch):
+    """Quantize the step's k and v [n_tokens, H, D] (bf16, any token stride)
+    into the cache."""
+    _heads(k, batch.n_tokens, cache.H, cache.D, "k")
+    _heads(v, batch.n_tokens, cache.H, cache.D, "v")
+    _check(lib().gnf4_kv_cache_write(ctypes.byref(cache.cstruct()), ctypes.byref(batch.cstruct()), k.data_ptr(),
+                                     _tstride(k), v.data_ptr(), _tstride(v), _stream()), "gnf4_kv_cache_write")
+
+
+def kv_cache_read(cache, batch, dtype=torch.bfloat16, k=None, v=None):
+    """The values of the step's rows, (k, v) [n_tokens, H, D] in bf16 or
+    float32. Rows that are not in the cache are left as they are (uninitialised
+    when k and v are allocated here)."""
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("dtype must be bfloat16 or float32")
+    shape = (batch.n_tokens, cache.H, cache.D)
+    k = torch.empty(shape, dtype=dtype, device=cache.k_codes.device) if k is None else _here(k, dtype, "k")
+    v = torch.empty(shape, dtype=dtype, device=cache.k_codes.device) if v is None else _here(v, dtype, "v")
+    if k.shape != shape or v.shape != shape:
+        raise ValueError("k and v must be [n_tokens, H, D]")
+    _check(lib().gnf4_kv_cache_read(ctypes.byref(cache.cstruct()), ctypes.byref(batch.cstruct()),
+                                    int(dtype == torch.float32), k.data_ptr(), v.data_ptr(), _stream()),
+           "gnf4_kv_cache_read")
+    return k, v
+
+
+def kv_attention_workspace_bytes(cache, batch, Hq, window=0):
+    return int(lib().gnf4_kv_attention_workspace_bytes(ctypes.byref(cache.cstruct()), ctypes.byref(batch.cstruct()),
+                                                       Hq, window))
+
+
+def kv_attention(q, cache, batch, scale=None, window=0, sinks=None, out=None, lse=None, workspace=None):
+    """Attention of q [n_tokens, Hq, D] (bf16, any token stride) over the cache:
+    out [n_tokens, Hq, D] bf16. scale None: 1/sqrt(D); window 0: all earlier
+    positions; sinks float32 [Hq]; lse float32 [n_tokens, Hq] is filled when
+    given. Rows that belong to no sequence are left as they are (uninitialised
+    when out is allocated here)."""
+    T, Hq, D = batch.n_tokens, q.shape[1], cache.D
+    _heads(q, T, Hq, D, "q")
+    out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device) if out is None else _heads(out, T, Hq, D, "out")
+    if sinks is not None and _here(sinks, torch.float32, "sinks").numel() != Hq:
+        raise ValueError("sinks must hold Hq = %d values" % Hq)
+    if lse is not None and _here(lse, torch.float32, "lse").numel() != T * Hq:
+        raise ValueError("lse must be [n_tokens, Hq]")
+    cc, cb, L = ctypes.byref(cache.cstruct()), ctypes.byref(batch.cstruct()), lib()
+    if workspace is None:
+        need = L.gnf4_kv_attention_workspace_bytes(cc, cb, Hq, window)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    _check(L.gnf4_kv_attention(q.data_ptr(), _tstride(q), cc, cb, Hq, D ** -0.5 if scale is None else scale, window,
+                               _ptr(sinks), out.data_ptr(), _tstride(out), _ptr(lse), _ptr(workspace),
+                               0 if workspace is None else workspace.numel() * workspace.element_size(), _stream()),
+           "gnf4_kv_attention")
+    return out

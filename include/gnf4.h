@@ -28,6 +28,13 @@
  *                          for a projection whose rows were gathered
  * and a layer whose experts stay in host RAM streams them through an HBM
  * cache before the route: gnf4_expert_cache_stage, gnf4_expert_cache_fill.
+ * The attention in front of the experts keeps its keys and values in the same
+ * 4-bit formats:
+ *   gnf4_qk_norm_rope    query and key heads: norm and rotation by position
+ *   gnf4_kv_cache_write  keys and values -> packed rows of a paged cache
+ *   gnf4_kv_attention    the queries over the packed rows, decoded in registers
+ * (gnf4_kv_cache_read decodes rows again, gnf4_qk_norm_rope_dx is the backward
+ * pass of the first).
  *
  * Conventions for every entry point:
  *  - All array pointers are DEVICE pointers owned by the caller; the library
@@ -427,6 +434,177 @@ gnf4_status gnf4_expert_cache_stage(const int32_t *topk_ids, int32_t T, int32_t 
 gnf4_status gnf4_expert_cache_fill(const gnf4_weights *host_w, const gnf4_weights *cache_w,
                                    const int32_t *copies, int32_t max_copies,
                                    gnf4_stream_t stream);
+
+/* ---------------------------------------------------------------- attention
+ *
+ * The pages run the packed experts behind a real attention (section cited at
+ * the top, demonstration paragraph) and list FP8 paged decode attention with
+ * sliding window, sinks and a custom scale among the package's tasks ("MoE
+ * Training on Consumer GPUs -- Loggetta & Cerin Amroth", Task guides table)
+ * without a formula; the calls below are this library's 4-bit form of it.
+ */
+
+/* Rotation by position. inv_freq: DEVICE float32 [rot_dim / 2]. The first
+ * rot_dim values of a head are rotated in pairs, pair i by the angle position
+ * * inv_freq[i]: values (2i, 2i + 1) when interleaved = 1, (i, i + rot_dim/2)
+ * when 0; both are multiplied by mscale. rot_dim % 16 == 0. */
+typedef struct {
+  int32_t rot_dim, interleaved;
+  const float *inv_freq;
+  float mscale;
+} gnf4_rope;
+
+/* A paged 4-bit cache of one layer. Page p holds page_size positions of all H
+ * heads:
+ *   codes   uint8 [n_pages][H][page_size][D/2]
+ *   scales  NF4: float32 absmax [n_pages][H][page_size][D/64]
+ *           MXFP4: uint8 e8m0 [n_pages][H][page_size][D/32]
+ * for the keys and for the values, nibble order and meaning as in
+ * gnf4_weights. format GNF4_NF4 or GNF4_MXFP4 (NF4_DQ's second-level scales
+ * span many rows, which are not written together: UNSUPPORTED); page_size a
+ * power of two in [16, 65536]; D 64, 128 or 256; 1 <= H <= 1024; all arrays
+ * 16-byte aligned. */
+typedef struct {
+  int32_t format, n_pages, page_size, H, D;
+  uint8_t *k_codes;
+  void *k_scales;
+  uint8_t *v_codes;
+  void *v_scales;
+} gnf4_kv_cache;
+
+/* The rows of one step. Sequence b's new tokens are rows [offsets[b],
+ * offsets[b+1]) of the step's [n_tokens][...] arrays, and lens[b] is its length
+ * with them: row r stands at position lens[b] - offsets[b+1] + r. Position p of
+ * sequence b lies on page pages[b * max_pages + p / page_size], place p %
+ * page_size. offsets int32 [B+1] ascending, lens int32 [B], pages int32
+ * [B][max_pages], all on the device; max_pages * page_size <= 2^30; B <= 2^20.
+ * max_new (>= 1) is a bound on the new tokens of any one sequence: attention
+ * does not compute rows past it. max_len is the longest length expected: it
+ * decides how the work is split, and longer sequences are still computed
+ * whole. Nothing is read back, so what the arrays say is taken as it is:
+ *  - rows of [0, n_tokens) that belong to no sequence (before offsets[0],
+ *    behind offsets[B]) are left as they are by every call;
+ *  - a position below 0 or past max_pages * page_size, or whose page id lies
+ *    outside [0, n_pages), does not exist: it is not written, not read (the
+ *    output row is left as it is) and not attended to.
+ * The pages a call writes to must not be shared by positions it writes: two
+ * rows on the same place leave bytes of both. */
+typedef struct {
+  int32_t B, n_tokens, max_new, max_len;
+  const int32_t *offsets, *lens, *pages;
+  int32_t max_pages;
+} gnf4_kv_batch;
+
+typedef enum { GNF4_ROPE_PLAIN = 0, GNF4_ROPE_LINEAR = 1, GNF4_ROPE_YARN = 2 } gnf4_rope_scaling;
+
+/* gnf4_rope_frequencies -- the frequency table of a rotation, on the HOST (to
+ * be copied to the device): inv_freq[i] = base^(-2 i / rot_dim), i < rot_dim/2,
+ * formed in float64 and rounded once, and, for contexts longer than trained,
+ *   LINEAR  divided by factor;
+ *   YARN    (NTK-by-parts interpolation, Peng et al. 2023): with r = the turns
+ *           original_len * inv_freq / (2 pi) and g = clamp((r - beta_slow) /
+ *           (beta_fast - beta_slow), 0, 1), inv_freq * (g + (1 - g) / factor);
+ *           *mscale = 0.1 ln(factor) + 1 (1 for the other two).
+ * rot_dim a positive multiple of 2 up to 256, base > 1, factor >= 1,
+ * original_len > 0 and 0 <= beta_slow < beta_fast for YARN; mscale may be
+ * NULL. */
+gnf4_status gnf4_rope_frequencies(int32_t rot_dim, double base, int32_t scaling, double factor,
+                                  double original_len, double beta_fast, double beta_slow,
+                                  float *inv_freq, float *mscale);
+
+/* gnf4_qk_norm_rope -- norm of every query and key head and the rotation by
+ * position, one launch. For each of the Hq heads x of q[t] and Hk heads of
+ * k[t], D values each:
+ *   n = x / sqrt(mean(x^2) + eps) * w     (w = wq or wk; NULL: n = x)
+ *   out = bf16(rotation of n at positions[t])   (rope NULL: bf16(n))
+ * in float32 with the angle position * inv_freq in float64; rounded once.
+ * q, k, q_out, k_out: bf16 bits, token t at t * stride elements, heads
+ * [H][D] within; strides multiples of 8, at least H * D (they let q and k be
+ * parts of one projection's rows); pointers 16-byte aligned. wq, wk bf16 [D],
+ * 16-byte aligned. positions int32 [T] (negative ones rotate backwards).
+ * q_out may be q and k_out k with the same stride; otherwise inputs and
+ * outputs must not overlap. One of Hq, Hk may be 0 (its pointers are then not
+ * used). D % 8 == 0, 16 <= D <= 256; rot_dim <= D; eps >= 0. T = 0 is a no-op;
+ * at most 2^31 - 1 tokens, 65535 heads. */
+gnf4_status gnf4_qk_norm_rope(const uint16_t *q, int64_t q_stride, const uint16_t *k,
+                              int64_t k_stride, int32_t T, int32_t Hq, int32_t Hk, int32_t D,
+                              const uint16_t *wq, const uint16_t *wk, float eps,
+                              const gnf4_rope *rope, const int32_t *positions, uint16_t *q_out,
+                              int64_t q_out_stride, uint16_t *k_out, int64_t k_out_stride,
+                              gnf4_stream_t stream);
+
+/* gnf4_qk_norm_rope_dx -- backward pass of gnf4_qk_norm_rope: from dq, dk (bf16,
+ * the gradients of q_out, k_out) and the forward's q, k,
+ *   g = transposed rotation of dq;  z = x / sqrt(mean(x^2) + eps)
+ *   dwq[i] = sum over t and heads of g[i] * z[i]              float32 [D]
+ *   h = g * w;  gq = bf16((h - z * mean(h * z)) / sqrt(mean(x^2) + eps))
+ * and the same for the keys (w NULL: gq = bf16(g), q not read). dwq / dwk may
+ * be NULL (not computed) and must be NULL where wq / wk is. gq may be dq and gk
+ * dk with the same stride. Sums in float32 in a fixed order: two calls with the
+ * same arguments give the same bits. workspace:
+ * gnf4_qk_norm_rope_dx_workspace_bytes(T, D) device bytes, 16-byte aligned,
+ * needed when dwq or dwk is given; contents do not matter. T = 0 writes zero
+ * weight gradients. Other arguments and limits as the forward. */
+gnf4_status gnf4_qk_norm_rope_dx(const uint16_t *dq, int64_t dq_stride, const uint16_t *dk,
+                                 int64_t dk_stride, const uint16_t *q, int64_t q_stride,
+                                 const uint16_t *k, int64_t k_stride, int32_t T, int32_t Hq,
+                                 int32_t Hk, int32_t D, const uint16_t *wq, const uint16_t *wk,
+                                 float eps, const gnf4_rope *rope, const int32_t *positions,
+                                 uint16_t *gq, int64_t gq_stride, uint16_t *gk, int64_t gk_stride,
+                                 float *dwq, float *dwk, void *workspace, size_t workspace_bytes,
+                                 gnf4_stream_t stream);
+
+/* Workspace bytes of the call above (0 for invalid arguments). */
+size_t gnf4_qk_norm_rope_dx_workspace_bytes(int32_t T, int32_t D);
+
+/* gnf4_kv_cache_write -- quantize the step's keys and values into their places:
+ * row r of k and v (bf16 [n_tokens][H][D], token strides in elements, multiples
+ * of 8 and at least H * D, 16-byte aligned) as gnf4_quantize packs a float32
+ * row (NF4: absmax per 64 and the nearest code, ties to the lower; MXFP4:
+ * shared exponent floor(log2 amax) - 2, nearest even, saturating at 6). A
+ * block that holds a NaN or an infinity reads back as NaN throughout. */
+gnf4_status gnf4_kv_cache_write(const gnf4_kv_cache *cache, const gnf4_kv_batch *batch,
+                                const uint16_t *k, int64_t k_stride, const uint16_t *v,
+                                int64_t v_stride, gnf4_stream_t stream);
+
+/* gnf4_kv_cache_read -- the values the step's rows hold in the cache: k, v
+ * [n_tokens][H][D], float32 (gnf4_dequant's value) when out_f32 = 1, else bf16
+ * bits of it (nearest even; NaN gives 0x7FC0); 16-byte aligned. A batch with
+ * offsets = the running sums of lens reads whole sequences. */
+gnf4_status gnf4_kv_cache_read(const gnf4_kv_cache *cache, const gnf4_kv_batch *batch,
+                               int32_t out_f32, void *k, void *v, gnf4_stream_t stream);
+
+/* gnf4_kv_attention -- attention of the step's queries over the cache:
+ *   out[r][hq] = bf16(sum_p w_p v[p][h]),  h = hq / (Hq / H),
+ *   w_p = exp(x_p - m) / (sum_p exp(x_p - m) + exp(sinks[hq] - m)),
+ *   x_p = scale * (q[r][hq] . k[p][h])
+ * over the positions p that row r sees: 0 <= p <= its own, p > own - window
+ * when window > 0, on an existing page; the sink term only when sinks (float32
+ * [Hq]) is given. k, v are the decoded values. A row that sees nothing gives 0
+ * (lse: -inf, or the sink). What lies in places a row does not see (stale or
+ * unwritten bytes, NaN) does not reach it. lse (float32 [n_tokens][Hq], may
+ * be NULL) receives m + log of the denominator, by which results over separate
+ * parts of a context can be joined.
+ * q, out: bf16 bits [n_tokens][Hq][D] with token strides (multiples of 8, at
+ * least Hq * D), 16-byte aligned; they must not overlap. Hq % H == 0, Hq <=
+ * 65536. The cache holds a row before its query attends to it, so the write
+ * comes first on the stream.
+ * Arithmetic: products of bf16 operands with float32 sums. MXFP4 values are
+ * exact in bf16; NF4 enters as the bf16 operand codebook of the GEMMs with the
+ * absmax applied in float32; probabilities are rounded to bf16 for the second
+ * product. Deterministic. workspace: gnf4_kv_attention_workspace_bytes device
+ * bytes for the same arguments, 16-byte aligned (NULL when 0), contents
+ * unimportant; calls that may overlap need one each. One launch, or two when
+ * the positions of a row tile are split over workgroups. */
+gnf4_status gnf4_kv_attention(const uint16_t *q, int64_t q_stride, const gnf4_kv_cache *cache,
+                              const gnf4_kv_batch *batch, int32_t Hq, float scale, int32_t window,
+                              const float *sinks, uint16_t *out, int64_t out_stride, float *lse,
+                              void *workspace, size_t workspace_bytes, gnf4_stream_t stream);
+
+/* Workspace bytes of the call above (0 also for invalid arguments); only the
+ * sizes in cache and batch are used. */
+size_t gnf4_kv_attention_workspace_bytes(const gnf4_kv_cache *cache, const gnf4_kv_batch *batch,
+                                         int32_t Hq, int32_t window);
 
 /* gnf4_read_probe -- the achievable HBM read rate of the device, the
  * ceiling the decode GEMV's packed-weight bandwidth is compared with (the

@@ -1,0 +1,320 @@
+"""GPU parity of attention over the paged 4-bit cache with the float64 oracle,
+and the whole path norm + rotation -> cache write -> attention."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import attention as oa
+
+from .attention_util import (EPS8, Step, attention_bars, check_attention, dev, dev_bf16, device_cache, to_bf16, values)
+from .gpu_util import gnf4, say
+
+pytestmark = pytest.mark.gpu
+
+FMTS = ["nf4", "mxfp4"]
+
+
+def filled(fmt, step, H, D, seed, sharp=1.0):
+    """An oracle cache holding every position of the step's sequences; what lies
+    elsewhere is NaN scales and random codes."""
+    r = np.random.default_rng([seed, H, D, step.page])
+    c = oa.Cache(fmt, step.n_pages, step.page, H, D)
+    for side in range(2):
+        c.codes[side][:] = r.integers(0, 256, c.codes[side].shape)
+        c.scales[side][:] = 255 if fmt == "mxfp4" else np.nan
+    whole = step.whole()
+    k, v = r.standard_normal((2, whole.T, H, D))
+    k[..., ::19] *= 2.0
+    c.write(whole.oracle(), sharp * k, v)
+    return c
+
+
+def queries(T, Hq, D, seed):
+    return to_bf16(np.random.default_rng([T, Hq, D, seed]).standard_normal((T, Hq, D)))
+
+
+def run(fmt, step, H, G, D, window=0, sinks=False, scale=None, seed=0, sharp=1.0, cache=None, q=None):
+    g = gnf4()
+    say("kv_attention", fmt, "lens", step.lens[:6], "new", step.new[:6], "page", step.page, "H", H, "G", G, "D", D,
+        "window", window, "sinks", sinks)
+    c = filled(fmt, step, H, D, seed, sharp) if cache is None else cache
+    bits, qv = queries(step.T, H * G, D, seed) if q is None else q
+    sk = np.random.default_rng(seed).standard_normal(H * G).astype(np.float32) if sinks else None
+    sc = D ** -0.5 if scale is None else scale
+    lse = torch.full((step.T, H * G), 5.0, device="cuda")
+    out = torch.full((step.T, H * G, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    g.kv_attention(dev_bf16(bits), device_cache(g, c), step.device(g), scale, window, None if sk is None else dev(sk),
+                   out, lse)
+    torch.cuda.synchronize()
+    ref = oa.attend(qv, c, step.oracle(), float(np.float32(sc)), window, sk)
+    rows = sorted(r for r, _, _ in step.oracle().rows())
+    worst = check_attention(fmt, values(out), lse.cpu().numpy().astype(np.float64), ref, rows)
+    left = sorted(set(range(step.T)) - set(rows))
+    assert torch.all(out[left] == 7.0) and torch.all(lse[left] == 5.0)
+    return worst, out
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("G", [1, 4, 8])
+def test_decode_lengths(fmt, D, G):
+    """One new token at lengths around every border of a tile, a round and a page."""
+    lens = [1, 2, 15, 16, 17, 31, 32, 33, 127, 128, 129, 300]
+    run(fmt, Step(lens, [1] * len(lens), 16), 2, G, D)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("G,new", [(1, 1), (3, 5), (16, 1), (16, 2), (5, 7), (8, 17), (7, 1), (1, 64), (1, 65), (64, 1), (40, 3)])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_row_tiles(fmt, G, new, D):
+    """Every count of 16-row tiles, rows that do not fill one, several tiles, causal among the new tokens."""
+    run(fmt, Step([new + 40, new, new + 3], [new, new, max(new - 1, 0)], 32), 1 if G > 8 else 2, G, D)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("page", [16, 32, 64, 256])
+def test_pages(fmt, page):
+    run(fmt, Step([page * 2 + 5, page, 3, page - 1], [2, 1, 3, 1], page, slack=3), 2, 4, 128)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("window", [1, 2, 31, 128, 200, 100000, 2 ** 31 - 1])
+@pytest.mark.parametrize("sinks", [False, True])
+def test_window_and_sinks(fmt, window, sinks):
+    run(fmt, Step([400, 5, 131, 260], [1, 5, 4, 70], 16), 1, 4, 64, window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_split_over_workgroups(fmt, D):
+    """Few rows over a long context: ranges of it in separate workgroups, joined."""
+    g = gnf4()
+    step = Step([3000, 900], [1, 1], 64)
+    c = filled(fmt, step, 1, D, 3)
+    assert g.kv_attention_workspace_bytes(device_cache(g, c), step.device(g), 8) > 0
+    run(fmt, step, 1, 8, D, cache=c, sinks=True)
+    run(fmt, Step([1500], [19], 32), 1, 3, D)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_lengths_beyond_the_bound(fmt):
+    """max_len only decides the split: sequences longer than it are computed whole."""
+    run(fmt, Step([700, 90, 260], [1, 1, 1], 16, max_len=100), 1, 4, 128)
+    run(fmt, Step([1700, 90], [1, 1], 16, max_len=600), 1, 4, 128)
+    run(fmt, Step([300, 90], [1, 1], 16, max_len=1 << 30), 1, 4, 128)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_empty_sequences_and_rows_that_see_nothing(fmt):
+    """Sequences without new tokens; lengths below the new tokens (rows at
+    negative positions); rows before and behind the sequences are left alone."""
+    for sinks in (False, True):
+        step = Step([30, 0, 12, 7], [2, 0, 0, 7], 16)
+        step.lens[3] = 4                                     # rows at -3 .. 3
+        step.offsets = [1, 3, 3, 3, 10]
+        step.T = 12
+        c = filled(fmt, Step([30, 0, 12, 7], [2, 0, 0, 7], 16), 2, 64, 4)
+        run(fmt, step, 2, 2, 64, sinks=sinks, cache=c)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_bad_pages_are_not_attended(fmt):
+    step = Step([200, 70], [3, 1], 16)
+    c = filled(fmt, step, 2, 128, 5)
+    for p in (2, 7):
+        step.pages[0, p] = -1
+    step.pages[0, 11] = step.n_pages
+    step.pages[1, :] = 1 << 30                               # sequence 1 sees nothing
+    _, out = run(fmt, step, 2, 4, 128, cache=c)
+    assert not out[3].any()
+    assert out[:3].any()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("side", [0, 1])
+def test_nan_reaches_only_rows_that_see_it(fmt, D, side):
+    """A NaN block at a position that some rows of a tile see and others do not,
+    and one inside a full tile."""
+    step = Step([300], [40], 16)
+    c = filled(fmt, step, 1, D, 6)
+    for pos in (280, 289):
+        at = c.place(step.oracle(), 0, pos)
+        c.scales[side][at[0], 0, at[1], -1] = 255 if fmt == "mxfp4" else np.nan
+    _, out = run(fmt, step, 1, 2, D, cache=c)
+    bad = torch.isnan(out).any(-1).any(-1).cpu().numpy()
+    assert list(bad) == [260 + i >= 280 for i in range(40)]
+    c = filled(fmt, step, 1, D, 6)
+    at = c.place(step.oracle(), 0, 20)
+    c.scales[side][at[0], 0, at[1], 0] = 255 if fmt == "mxfp4" else np.nan
+    _, out = run(fmt, step, 1, 2, D, cache=c)
+    assert torch.isnan(out).any(-1).all()
+    # the window has left position 20 behind for every row
+    _, out = run(fmt, step, 1, 2, D, cache=c, window=100)
+    assert not torch.isnan(out).any()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_special_queries(fmt):
+    """Infinite and NaN queries give NaN in their own row only; zero queries the mean."""
+    step = Step([50, 60], [3, 2], 16)
+    c = filled(fmt, step, 1, 64, 7)
+    bits, q = queries(5, 2, 64, 7)
+    q = q.copy()
+    q[0, 0, 3], q[1, 1, 9], q[2] = np.nan, np.inf, 0.0
+    bits, q = to_bf16(q)
+    g = gnf4()
+    say("kv_attention special queries", fmt)
+    out = g.kv_attention(dev_bf16(bits), device_cache(g, c), step.device(g))
+    assert torch.isnan(out).any(-1).nonzero().tolist() == [[0, 0], [1, 1]]
+    with np.errstate(invalid="ignore"):
+        ref = oa.attend(q, c, step.oracle(), 0.125)
+    bar, _ = attention_bars(fmt, *(ref[i] for i in (0, 2, 3)))
+    got = values(out)
+    for r, h in ((2, 0), (2, 1), (3, 0), (4, 1), (0, 1), (1, 0)):
+        assert np.all(np.abs(got[r, h] - ref[0][r, h]) <= bar[r, h])
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("scale", [0.0, -0.2, 1.0])
+def test_scales_and_peaked_rows(fmt, scale):
+    run(fmt, Step([150, 33], [2, 1], 16), 2, 4, 64, scale=scale)
+    run(fmt, Step([150, 33], [2, 1], 16), 2, 4, 64, sharp=4.0)
+
+
+def test_equal_heads_and_shuffled_pages_give_equal_bits():
+    """The result depends on what the pages hold, not on where they lie."""
+    g = gnf4()
+    say("kv_attention page order")
+    a, b = Step([500, 77], [1, 3], 32, seed=1), Step([500, 77], [1, 3], 32, seed=2, spare=9)
+    q = dev_bf16(queries(4, 16, 128, 1)[0])
+    outs = []
+    for s in (a, b):
+        c = oa.Cache("nf4", s.n_pages, 32, 2, 128)
+        r = np.random.default_rng(5)
+        c.write(s.whole().oracle(), *r.standard_normal((2, 577, 2, 128)))
+        outs.append(g.kv_attention(q, device_cache(g, c), s.device(g)))
+    assert torch.equal(*outs) and torch.equal(outs[0], g.kv_attention(q, device_cache(g, c), b.device(g)))
+
+
+def test_strides_and_int16_bits():
+    g = gnf4()
+    say("kv_attention strides")
+    step = Step([100, 260], [1, 4], 16)
+    c = filled("mxfp4", step, 2, 128, 9)
+    gc, b = device_cache(g, c), step.device(g)
+    bits, _ = queries(5, 8, 128, 9)
+    q = dev_bf16(bits)
+    want = g.kv_attention(q, gc, b)
+    wide = torch.zeros((5, 3000), dtype=torch.bfloat16, device="cuda")
+    wide[:, 8:8 + 1024] = q.view(5, 1024)
+    out = torch.full((5, 2000), 7.0, dtype=torch.bfloat16, device="cuda")
+    g.kv_attention(wide[:, 8:8 + 1024].view(5, 8, 128), gc, b, out=out[:, 16:16 + 1024].view(5, 8, 128))
+    assert torch.equal(out[:, 16:16 + 1024].view(5, 8, 128), want)
+    assert torch.all(out[:, :16] == 7) and torch.all(out[:, 16 + 1024:] == 7)
+    assert torch.equal(g.kv_attention(q.view(torch.int16), gc, b).view(torch.bfloat16), want)
+
+
+def test_decode_loop_through_a_graph_and_another_stream():
+    """Norm + rotation, write and attention of a decode step, captured once and
+    replayed while the sequences grow (new lengths and pages come in through
+    the same arrays), against eager steps on a second cache and stream."""
+    g = gnf4()
+    say("decode loop")
+    H, Hq, D, page, B, steps = 2, 8, 128, 16, 3, 5
+    r = np.random.default_rng(11)
+    start = np.array([14, 30, 3])
+    width = 4
+    pages = r.permutation(B * width).reshape(B, width).astype(np.int32)
+    off = dev(np.arange(B + 1, dtype=np.int32))
+    lens = dev((start + 1).astype(np.int32))
+    pos = dev(start.astype(np.int32))
+    batch = g.KVBatch(off, lens, dev(pages), B, 1, 64)
+    rope = g.rope_frequencies(D, 10000.0)
+    w = dev_bf16(to_bf16(1 + 0.1 * r.standard_normal(D))[0])
+    caches = [g.empty_kv_cache("nf4", B * width, page, H, D) for _ in range(2)]
+    whole = g.KVBatch(dev(np.concatenate(([0], np.cumsum(start))).astype(np.int32)), dev(start.astype(np.int32)),
+                      dev(pages), int(start.sum()), int(start.max()), 64)
+    k0, v0 = (dev_bf16(to_bf16(r.standard_normal((int(start.sum()), H, D)))[0]) for _ in range(2))
+    for c in caches:
+        g.kv_cache_write(c, k0, v0, whole)
+    x = torch.zeros((B, (Hq + 2 * H) * D), dtype=torch.bfloat16, device="cuda")
+    q, k, v = (x[:, a * D:b * D].view(B, b - a, D) for a, b in ((0, Hq), (Hq, Hq + H), (Hq + H, Hq + 2 * H)))
+
+    def step(cache):
+        qr, kr = g.qk_norm_rope(q, k, pos, rope, w, w)
+        g.kv_cache_write(cache, kr, v, batch)
+        return g.kv_attention(qr, cache, batch, sinks=None)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(caches[0])                                      # warm up; rewritten by the first replay
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(caches[0])
+    for i in range(steps):
+        x.copy_(dev_bf16(to_bf16(r.standard_normal(x.shape))[0]))
+        graph.replay()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            want = step(caches[1])
+        torch.cuda.current_stream().wait_stream(side)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and torch.isfinite(got).all(), i
+        lens += 1
+        pos += 1
+    n = int(lens.sum().item()) - B
+    end = g.KVBatch(dev(np.concatenate(([0], np.cumsum(start + steps))).astype(np.int32)), dev((start + steps).astype(np.int32)),
+                    dev(pages), n, 64, 64)
+    for a, b in zip(g.kv_cache_read(caches[0], end), g.kv_cache_read(caches[1], end)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_path_norm_write_attend_against_the_oracle(fmt):
+    """The three calls of a step chained on the device against the oracle's chain on the device's own rounded rows."""
+    g = gnf4()
+    say("path", fmt)
+    H, Hq, D = 2, 8, 64
+    step = Step([40, 9, 70], [40, 9, 70], 16)
+    r = np.random.default_rng(13)
+    pos = np.concatenate([np.arange(n) for n in step.lens]).astype(np.int32)
+    rope = g.rope_frequencies(D, 500.0, "linear", 2.0)
+    w = dev_bf16(to_bf16(1 + 0.1 * r.standard_normal(D))[0])
+    q, k, v = (to_bf16(r.standard_normal((step.T, h, D))) for h in (Hq, H, H))
+    qr, kr = g.qk_norm_rope(dev_bf16(q[0]), dev_bf16(k[0]), dev(pos), rope, w, w)
+    gc = g.empty_kv_cache(fmt, step.n_pages, 16, H, D)
+    b = step.device(g)
+    g.kv_cache_write(gc, kr, dev_bf16(v[0]), b)
+    out = g.kv_attention(qr, gc, b)
+    c = oa.Cache(fmt, step.n_pages, 16, H, D)
+    c.write(step.oracle(), values(kr), v[1])
+    ref = oa.attend(values(qr), c, step.oracle(), D ** -0.5)
+    check_attention(fmt, values(out), None, ref)
+    # and the rotated rows are those of the oracle within a bf16 step
+    f = rope.inv_freq.cpu().numpy()
+    want = oa.norm_rope(k[1], values(w), 1e-6, pos, f, False)
+    assert np.all(np.abs(values(kr) - want) <= EPS8 * np.abs(want) + 1e-5)
+
+
+def test_workspace_and_binding_refusals():
+    g = gnf4()
+    step = Step([3000], [1], 64)
+    c = filled("mxfp4", step, 1, 64, 1)
+    gc, b = device_cache(g, c), step.device(g)
+    q = dev_bf16(queries(1, 4, 64, 1)[0])
+    need = g.kv_attention_workspace_bytes(gc, b, 4)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")      # NaN everywhere: contents do not matter
+    assert torch.equal(g.kv_attention(q, gc, b, workspace=ws), g.kv_attention(q, gc, b))
+    with pytest.raises(g.Gnf4Error) as e:
+        g.kv_attention(q, gc, b, workspace=ws[:need - 16])
+    assert e.value.status == 3
+    with pytest.raises(ValueError):
+        g.kv_attention(q[:, :, :32], gc, b)
+    with pytest.raises(ValueError):
+        g.kv_attention(q, gc, b, sinks=torch.zeros(3, device="cuda"))
+    with pytest.raises(ValueError):
+        g.kv_attention(q, gc, b, lse=torch.zeros(4, dtype=torch.float64, device="cuda"))
