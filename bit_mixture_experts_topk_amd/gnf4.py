@@ -11,6 +11,7 @@ dequant, quantize, nf4_codebook, last_error, build_id.
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 from typing import Optional
 
@@ -106,8 +107,9 @@ def lib():
         L.gnf4_expert_cache_reset.argtypes = [P, I, I, S]
         L.gnf4_expert_cache_stage.argtypes = [P, I, I, I, I, P, P, P, S]
         L.gnf4_expert_cache_fill.argtypes = [ctypes.POINTER(CWeights), ctypes.POINTER(CWeights), P, I, S]
-        F, W, RP = ctypes.c_float, ctypes.c_int64, ctypes.POINTER(CRope)
-        D, CP, BP = ctypes.c_double, ctypes.POINTER(CKVCache), ctypes.POINTER(CKVBatch)
+        F, W = ctypes.c_float, ctypes.c_int64
+        # descriptors: a pointer to the structure, or its packed bytes
+        D, RP, CP, BP = ctypes.c_double, P, P, P
         L.gnf4_rope_frequencies.argtypes = [I, D, I, D, D, D, D, ctypes.POINTER(F), ctypes.POINTER(F)]
         L.gnf4_qk_norm_rope.argtypes = [P, W, P, W, I, I, I, I, P, P, F, RP, P, P, W, P, W, S]
         L.gnf4_qk_norm_rope_dx.argtypes = [P, W, P, W, P, W, P, W, I, I, I, I, P, P, F, RP, P, P, W, P, W,
@@ -541,6 +543,50 @@ def expert_cache_fill(host_w, cache_w, copies, max_copies):
 
 ROPE_SCALINGS = {"plain": 0, "linear": 1, "yarn": 2}
 
+# A decode step makes several of these calls per layer and each runs for a few
+# microseconds, so the binding's own time is kept down: descriptors are packed
+# as bytes (CRope, CKVCache, CKVBatch above give the fields) and every tensor
+# is looked at once.
+_BITS16 = frozenset((torch.bfloat16, torch.int16))
+_pack_rope = struct.Struct("@2iPf4x").pack
+_pack_cache = struct.Struct("@5i4x4P").pack
+_pack_batch = struct.Struct("@4i3Pi4x").pack
+_device = torch.cuda.current_device
+
+
+def _here(t, dtype, name, dev):
+    """Address of t, a contiguous tensor of that type on the current device."""
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        if t.is_cuda and t.get_device() != dev:
+            raise ValueError("%s lies on %s, which is not the current device" % (name, t.device))
+        raise ValueError("%s must be a contiguous %s CUDA tensor" % (name, dtype))
+    return t.data_ptr()
+
+
+def _heads(t, T, H, D, name, dev):
+    """Token stride of t, bf16 (or 16-bit pattern) [T, H, D] on the current
+    device with each token's heads contiguous."""
+    if t.dtype not in _BITS16 or t.get_device() != dev or t.shape != (T, H, D):
+        if t.is_cuda and t.get_device() != dev:
+            raise ValueError("%s lies on %s, which is not the current device" % (name, t.device))
+        raise ValueError("%s must be a bf16 (or 16-bit bit pattern) CUDA tensor [%d, %d, %d]" % (name, T, H, D))
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 or (s1 != D and H > 1)) and T * H:
+        raise ValueError("the heads of %s must be contiguous within a token" % name)
+    return s0 if T > 1 else H * D                            # a single token: its own size
+
+
+def _weight(w, D, name, dev):
+    if w is None:
+        return None
+    if w.dtype not in _BITS16 or w.numel() != D:
+        raise ValueError("%s must hold D = %d bf16 values" % (name, D))
+    return _here(w, w.dtype, name, dev)
+
+
+def _raw_stream(dev):
+    return torch._C._cuda_getCurrentRawStream(dev)
+
 
 @dataclass
 class Rope:
@@ -551,8 +597,9 @@ class Rope:
     interleaved: bool = False
     mscale: float = 1.0
 
-    def cstruct(self):
-        return CRope(2 * self.inv_freq.numel(), int(self.interleaved), self.inv_freq.data_ptr(), self.mscale)
+    def packed(self, dev):
+        f = self.inv_freq
+        return _pack_rope(2 * f.numel(), bool(self.interleaved), _here(f, torch.float32, "inv_freq", dev), self.mscale)
 
 
 @dataclass
@@ -569,17 +616,16 @@ class KVCache:
     v_codes: torch.Tensor
     v_scales: torch.Tensor
 
-    def cstruct(self):
-        codes, scales = (self.k_codes, self.v_codes), (self.k_scales, self.v_scales)
-        rows = self.n_pages * self.H * self.page_size
+    def packed(self, dev):
         mx = self.format == MXFP4
-        for c, s in zip(codes, scales):
-            _here(c, torch.uint8, "cache codes")
-            _here(s, torch.uint8 if mx else torch.float32, "cache scales")
-            if c.numel() != rows * (self.D // 2) or s.numel() != rows * (self.D // (32 if mx else 64)):
-                raise ValueError("the cache arrays do not hold n_pages * H * page_size rows of D values")
-        return CKVCache(self.format, self.n_pages, self.page_size, self.H, self.D, codes[0].data_ptr(),
-                        scales[0].data_ptr(), codes[1].data_ptr(), scales[1].data_ptr())
+        kc, ks, vc, vs = self.k_codes, self.k_scales, self.v_codes, self.v_scales
+        rows, kind = self.n_pages * self.H * self.page_size, torch.uint8 if mx else torch.float32
+        nc, ns = rows * (self.D // 2), rows * (self.D // (32 if mx else 64))
+        if kc.numel() != nc or vc.numel() != nc or ks.numel() != ns or vs.numel() != ns:
+            raise ValueError("the cache arrays do not hold n_pages * H * page_size rows of D values")
+        return _pack_cache(self.format, self.n_pages, self.page_size, self.H, self.D,
+                           _here(kc, torch.uint8, "k_codes", dev), _here(ks, kind, "k_scales", dev),
+                           _here(vc, torch.uint8, "v_codes", dev), _here(vs, kind, "v_scales", dev))
 
     def nbytes(self):
         return sum(t.numel() * t.element_size() for t in (self.k_codes, self.k_scales, self.v_codes, self.v_scales))
@@ -598,42 +644,13 @@ class KVBatch:
     max_new: int
     max_len: int
 
-    def cstruct(self):
-        for name in ("offsets", "lens", "pages"):
-            _here(getattr(self, name), torch.int32, name)
-        B = self.lens.numel()
-        if self.offsets.numel() != B + 1 or self.pages.dim() != 2 or self.pages.shape[0] != B:
+    def packed(self, dev):
+        B, shape = self.lens.numel(), self.pages.shape
+        if self.offsets.numel() != B + 1 or len(shape) != 2 or shape[0] != B:
             raise ValueError("offsets must hold B + 1, lens B and pages B rows of ids")
-        return CKVBatch(B, self.n_tokens, self.max_new, self.max_len, self.offsets.data_ptr(),
-                        self.lens.data_ptr(), self.pages.data_ptr(), self.pages.shape[1])
-
-
-def _here(t, dtype, name):
-    """t: a contiguous tensor of that type on the current device."""
-    if not (t.is_cuda and t.dtype == dtype and t.is_contiguous()):
-        raise ValueError("%s must be a contiguous %s CUDA tensor" % (name, dtype))
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError("%s lies on %s, which is not the current device" % (name, t.device))
-    return t
-
-
-def _heads(t, T, H, D, name):
-    """t: bf16 (or 16-bit pattern) [T, H, D] on the current device, any token stride."""
-    if not (t.is_cuda and t.element_size() == 2 and t.dim() == 3 and t.shape == (T, H, D)):
-        raise ValueError("%s must be a bf16 (or 16-bit bit pattern) CUDA tensor [%d, %d, %d]" % (name, T, H, D))
-    if t.dtype == torch.float16:
-        raise ValueError("%s is float16, not bf16" % name)
-    s = t.stride()
-    if t.numel() and (s[2] != 1 or (s[1] != D and H > 1)):
-        raise ValueError("the heads of %s must be contiguous within a token" % name)
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError("%s lies on %s, which is not the current device" % (name, t.device))
-    return t
-
-
-def _tstride(t):
-    """Token stride in elements (of a single token: its own size)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+        return _pack_batch(B, self.n_tokens, self.max_new, min(self.max_len, 0x7fffffff),
+                           _here(self.offsets, torch.int32, "offsets", dev), _here(self.lens, torch.int32, "lens", dev),
+                           _here(self.pages, torch.int32, "pages", dev), shape[1])
 
 
 def rope_frequencies(rot_dim, base=10000.0, scaling="plain", factor=1.0, original_len=0.0, beta_fast=32.0,
@@ -645,34 +662,36 @@ def rope_frequencies(rot_dim, base=10000.0, scaling="plain", factor=1.0, origina
     return Rope(torch.tensor(list(f), dtype=torch.float32, device=device), interleaved, m.value)
 
 
-def _rope_call(positions, rope, T, wq, wk, D):
-    if rope is not None:
-        _here(rope.inv_freq, torch.float32, "inv_freq")
-        _here(positions, torch.int32, "positions")
-        if positions.numel() != T:
-            raise ValueError("positions must hold T = %d values" % T)
-    for w, name in ((wq, "wq"), (wk, "wk")):
-        if w is not None and (w.numel() != D or w.element_size() != 2 or w.dtype == torch.float16):
-            raise ValueError("%s must hold D = %d bf16 values" % (name, D))
-        if w is not None:
-            _here(w, w.dtype, name)
-    return None if rope is None else ctypes.byref(rope.cstruct())
+def _positions(positions, rope, T, dev):
+    """(packed rotation, address of the positions), or nothing."""
+    if rope is None:
+        return None, None
+    if positions.numel() != T:
+        raise ValueError("positions must hold T = %d values" % T)
+    return rope.packed(dev), _here(positions, torch.int32, "positions", dev)
+
+
+def _result(out, like, T, H, D, name, dev):
+    """(tensor, token stride) of a result [T, H, D]: the given one, or a new one."""
+    if out is None:
+        return torch.empty((T, H, D), dtype=like.dtype, device=like.device), H * D
+    return out, _heads(out, T, H, D, name, dev)
 
 
 def qk_norm_rope(q, k, positions, rope=None, wq=None, wk=None, eps=1e-6, q_out=None, k_out=None):
     """Norm (bf16 weights wq, wk [D]; None: no norm) and rotation (None: none)
     of q [T, Hq, D] and k [T, Hk, D] (bf16, any token stride) at int32
     positions [T]; returns (q_out, k_out), which may be q and k themselves."""
+    dev = _device()
     T, Hq, D = q.shape
     Hk = k.shape[1]
-    _heads(q, T, Hq, D, "q")
-    _heads(k, T, Hk, D, "k")
-    r = _rope_call(positions, rope, T, wq, wk, D)
-    q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device) if q_out is None else _heads(q_out, T, Hq, D, "q_out")
-    k_out = torch.empty((T, Hk, D), dtype=k.dtype, device=k.device) if k_out is None else _heads(k_out, T, Hk, D, "k_out")
-    _check(lib().gnf4_qk_norm_rope(q.data_ptr(), _tstride(q), k.data_ptr(), _tstride(k), T, Hq, Hk, D, _ptr(wq), _ptr(wk),
-                                   eps, r, _ptr(positions), q_out.data_ptr(), _tstride(q_out), k_out.data_ptr(),
-                                   _tstride(k_out), _stream()), "gnf4_qk_norm_rope")
+    qs, ks = _heads(q, T, Hq, D, "q", dev), _heads(k, T, Hk, D, "k", dev)
+    r, pos = _positions(positions, rope, T, dev)
+    q_out, qos = _result(q_out, q, T, Hq, D, "q_out", dev)
+    k_out, kos = _result(k_out, k, T, Hk, D, "k_out", dev)
+    _check(lib().gnf4_qk_norm_rope(q.data_ptr(), qs, k.data_ptr(), ks, T, Hq, Hk, D, _weight(wq, D, "wq", dev),
+                                   _weight(wk, D, "wk", dev), eps, r, pos, q_out.data_ptr(), qos, k_out.data_ptr(), kos,
+                                   _raw_stream(dev)), "gnf4_qk_norm_rope")
     return q_out, k_out
 
 
@@ -681,25 +700,27 @@ def qk_norm_rope_dx(dq, dk, q, k, positions, rope=None, wq=None, wk=None, eps=1e
     """Backward pass of qk_norm_rope: (gq, gk, dwq, dwk) from the gradients dq,
     dk of its results and its inputs; dwq / dwk float32 [D], None without a
     weight. gq and gk may be dq and dk."""
+    dev = _device()
     T, Hq, D = dq.shape
     Hk = dk.shape[1]
-    _heads(dq, T, Hq, D, "dq")
-    _heads(dk, T, Hk, D, "dk")
-    _heads(q, T, Hq, D, "q")
-    _heads(k, T, Hk, D, "k")
-    r = _rope_call(positions, rope, T, wq, wk, D)
-    gq = torch.empty((T, Hq, D), dtype=dq.dtype, device=dq.device) if gq is None else _heads(gq, T, Hq, D, "gq")
-    gk = torch.empty((T, Hk, D), dtype=dk.dtype, device=dk.device) if gk is None else _heads(gk, T, Hk, D, "gk")
-    dwq = torch.empty(D, dtype=torch.float32, device=dq.device) if wq is not None else None
-    dwk = torch.empty(D, dtype=torch.float32, device=dq.device) if wk is not None else None
-    if workspace is None and (wq is not None or wk is not None):
-        workspace = torch.empty(lib().gnf4_qk_norm_rope_dx_workspace_bytes(T, D), dtype=torch.uint8, device=dq.device)
-    _check(lib().gnf4_qk_norm_rope_dx(dq.data_ptr(), _tstride(dq), dk.data_ptr(), _tstride(dk), q.data_ptr(), _tstride(q),
-                                      k.data_ptr(), _tstride(k), T, Hq, Hk, D, _ptr(wq), _ptr(wk), eps, r,
-                                      _ptr(positions), gq.data_ptr(), _tstride(gq), gk.data_ptr(), _tstride(gk),
-                                      _ptr(dwq), _ptr(dwk), _ptr(workspace),
-                                      0 if workspace is None else workspace.numel() * workspace.element_size(),
-                                      _stream()), "gnf4_qk_norm_rope_dx")
+    dqs, dks = _heads(dq, T, Hq, D, "dq", dev), _heads(dk, T, Hk, D, "dk", dev)
+    qs, ks = _heads(q, T, Hq, D, "q", dev), _heads(k, T, Hk, D, "k", dev)
+    r, pos = _positions(positions, rope, T, dev)
+    pq, pk = _weight(wq, D, "wq", dev), _weight(wk, D, "wk", dev)
+    gq, gqs = _result(gq, dq, T, Hq, D, "gq", dev)
+    gk, gks = _result(gk, dk, T, Hk, D, "gk", dev)
+    dwq = dwk = None
+    L, wsp, wsn = lib(), None, 0
+    if pq is not None or pk is not None:
+        dw = torch.empty((2, D), dtype=torch.float32, device=dq.device)
+        dwq, dwk = dw[0] if pq is not None else None, dw[1] if pk is not None else None
+        if workspace is None:
+            workspace = torch.empty(L.gnf4_qk_norm_rope_dx_workspace_bytes(T, D), dtype=torch.uint8, device=dq.device)
+        wsp, wsn = _here(workspace, workspace.dtype, "workspace", dev), workspace.numel() * workspace.element_size()
+    _check(L.gnf4_qk_norm_rope_dx(dq.data_ptr(), dqs, dk.data_ptr(), dks, q.data_ptr(), qs, k.data_ptr(), ks, T, Hq, Hk,
+                                  D, pq, pk, eps, r, pos, gq.data_ptr(), gqs, gk.data_ptr(), gks,
+                                  dwq.data_ptr() if dwq is not None else None, dwk.data_ptr() if dwk is not None else None,
+                                  wsp, wsn, _raw_stream(dev)), "gnf4_qk_norm_rope_dx")
     return gq, gk, dwq, dwk
 
 
@@ -716,32 +737,36 @@ def empty_kv_cache(fmt, n_pages, page_size, H, D, device="cuda"):
 def kv_cache_write(cache, k, v, batch):
     """Quantize the step's k and v [n_tokens, H, D] (bf16, any token stride)
     into the cache."""
-    _heads(k, batch.n_tokens, cache.H, cache.D, "k")
-    _heads(v, batch.n_tokens, cache.H, cache.D, "v")
-    _check(lib().gnf4_kv_cache_write(ctypes.byref(cache.cstruct()), ctypes.byref(batch.cstruct()), k.data_ptr(),
-                                     _tstride(k), v.data_ptr(), _tstride(v), _stream()), "gnf4_kv_cache_write")
+    dev = _device()
+    T, H, D = batch.n_tokens, cache.H, cache.D
+    ks, vs = _heads(k, T, H, D, "k", dev), _heads(v, T, H, D, "v", dev)
+    _check(lib().gnf4_kv_cache_write(cache.packed(dev), batch.packed(dev), k.data_ptr(), ks, v.data_ptr(), vs,
+                                     _raw_stream(dev)), "gnf4_kv_cache_write")
 
 
 def kv_cache_read(cache, batch, dtype=torch.bfloat16, k=None, v=None):
     """The values of the step's rows, (k, v) [n_tokens, H, D] in bf16 or
     float32. Rows that are not in the cache are left as they are (uninitialised
     when k and v are allocated here)."""
-    if dtype not in (torch.bfloat16, torch.float32):
+    dev = _device()
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
         raise ValueError("dtype must be bfloat16 or float32")
+    cc, cb = cache.packed(dev), batch.packed(dev)
     shape = (batch.n_tokens, cache.H, cache.D)
-    k = torch.empty(shape, dtype=dtype, device=cache.k_codes.device) if k is None else _here(k, dtype, "k")
-    v = torch.empty(shape, dtype=dtype, device=cache.k_codes.device) if v is None else _here(v, dtype, "v")
+    if k is None:
+        k = torch.empty(shape, dtype=dtype, device=cache.k_codes.device)
+    if v is None:
+        v = torch.empty(shape, dtype=dtype, device=cache.k_codes.device)
     if k.shape != shape or v.shape != shape:
         raise ValueError("k and v must be [n_tokens, H, D]")
-    _check(lib().gnf4_kv_cache_read(ctypes.byref(cache.cstruct()), ctypes.byref(batch.cstruct()),
-                                    int(dtype == torch.float32), k.data_ptr(), v.data_ptr(), _stream()),
-           "gnf4_kv_cache_read")
+    _check(lib().gnf4_kv_cache_read(cc, cb, dtype is torch.float32, _here(k, dtype, "k", dev), _here(v, dtype, "v", dev),
+                                    _raw_stream(dev)), "gnf4_kv_cache_read")
     return k, v
 
 
 def kv_attention_workspace_bytes(cache, batch, Hq, window=0):
-    return int(lib().gnf4_kv_attention_workspace_bytes(ctypes.byref(cache.cstruct()), ctypes.byref(batch.cstruct()),
-                                                       Hq, window))
+    dev = _device()
+    return int(lib().gnf4_kv_attention_workspace_bytes(cache.packed(dev), batch.packed(dev), Hq, window))
 
 
 def kv_attention(q, cache, batch, scale=None, window=0, sinks=None, out=None, lse=None, workspace=None):
@@ -750,19 +775,24 @@ def kv_attention(q, cache, batch, scale=None, window=0, sinks=None, out=None, ls
     positions; sinks float32 [Hq]; lse float32 [n_tokens, Hq] is filled when
     given. Rows that belong to no sequence are left as they are (uninitialised
     when out is allocated here)."""
+    dev = _device()
     T, Hq, D = batch.n_tokens, q.shape[1], cache.D
-    _heads(q, T, Hq, D, "q")
-    out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device) if out is None else _heads(out, T, Hq, D, "out")
-    if sinks is not None and _here(sinks, torch.float32, "sinks").numel() != Hq:
-        raise ValueError("sinks must hold Hq = %d values" % Hq)
-    if lse is not None and _here(lse, torch.float32, "lse").numel() != T * Hq:
-        raise ValueError("lse must be [n_tokens, Hq]")
-    cc, cb, L = ctypes.byref(cache.cstruct()), ctypes.byref(batch.cstruct()), lib()
+    qs = _heads(q, T, Hq, D, "q", dev)
+    out, outs = _result(out, q, T, Hq, D, "out", dev)
+    if sinks is not None:
+        if sinks.numel() != Hq:
+            raise ValueError("sinks must hold Hq = %d values" % Hq)
+        sinks = _here(sinks, torch.float32, "sinks", dev)
+    if lse is not None:
+        if lse.numel() != T * Hq:
+            raise ValueError("lse must be [n_tokens, Hq]")
+        lse = _here(lse, torch.float32, "lse", dev)
+    cc, cb, L, wsp, wsn = cache.packed(dev), batch.packed(dev), lib(), None, 0
     if workspace is None:
         need = L.gnf4_kv_attention_workspace_bytes(cc, cb, Hq, window)
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-    _check(L.gnf4_kv_attention(q.data_ptr(), _tstride(q), cc, cb, Hq, D ** -0.5 if scale is None else scale, window,
-                               _ptr(sinks), out.data_ptr(), _tstride(out), _ptr(lse), _ptr(workspace),
-                               0 if workspace is None else workspace.numel() * workspace.element_size(), _stream()),
-           "gnf4_kv_attention")
+    if workspace is not None:
+        wsp, wsn = _here(workspace, workspace.dtype, "workspace", dev), workspace.numel() * workspace.element_size()
+    _check(L.gnf4_kv_attention(q.data_ptr(), qs, cc, cb, Hq, D ** -0.5 if scale is None else scale, window, sinks,
+                               out.data_ptr(), outs, lse, wsp, wsn, _raw_stream(dev)), "gnf4_kv_attention")
     return out

@@ -222,9 +222,9 @@ def test_binding_refusals():
     with pytest.raises(ValueError):
         g.kv_cache_read(gc, b, torch.float16)
     with pytest.raises(ValueError):
-        g.KVCache(g.MXFP4, 4, 16, 2, 64, gc.k_codes, gc.k_scales, gc.v_codes, gc.v_scales).cstruct()
+        g.KVCache(g.MXFP4, 4, 16, 2, 64, gc.k_codes, gc.k_scales, gc.v_codes, gc.v_scales).packed(0)
     with pytest.raises(ValueError):
-        g.KVCache(g.NF4, 5, 16, 2, 64, gc.k_codes, gc.k_scales, gc.v_codes, gc.v_scales).cstruct()
+        g.KVCache(g.NF4, 5, 16, 2, 64, gc.k_codes, gc.k_scales, gc.v_codes, gc.v_scales).packed(0)
     with pytest.raises(ValueError):
         g.kv_cache_write(gc, x, x, g.KVBatch(b.offsets[:1], b.lens, b.pages, 5, 5, 5))
     with pytest.raises(g.Gnf4Error) as e:
