@@ -12,10 +12,13 @@
 //
 // Tiling. The query heads that share a cache head, for all new tokens of a
 // sequence, are the rows of one problem (row = token * G + g), cut into tiles
-// of 16 * NQ rows. A workgroup takes one tile, one cache head and a range of
-// positions; its four waves take 32 positions in turn (128 a round) and join
-// at the end through LDS. Ranges of one tile are joined by a second kernel.
-//
+// of 16 * NQ rows. A workgroup's NW waves take 32 positions each, 32 * NW a
+// round, and join at the end of a tile through LDS. NW is 8 where a wave's
+// registers allow two waves per SIMD, else 4.
+// Sequences differ in length, so the rounds of all (sequence, tile, head)
+// problems are numbered through and every workgroup, one per compute unit,
+// takes an equal run of them, over the end of one problem into the next. A
+// problem that lies in several runs is put together by a second kernel.
 // Registers only, no transposes. v_mfma_f32_16x16x32_bf16 takes A rows from
 // lanes 0..15 with 8 consecutive k per lane group g = lane / 16, and leaves C
 // with its column in the lane and rows 4g..4g+3 in the registers. Computed are
@@ -31,13 +34,13 @@
 // D/16 values of every one of 8 positions and pairs of positions are put
 // together after decoding.
 #include <algorithm>
+#include <type_traits>
 
 #include "kvcache.h"
 
 namespace gnf4 {
 
-constexpr int kAttnThreads = 256;
-constexpr int kAttnRound = 128;                 // positions per round of the four waves
+constexpr int kAttnGroups = 256;                // workgroups of a shared launch: the compute units
 constexpr float kNegInf = -__builtin_inff();
 
 __device__ __forceinline__ float max_xor16_32(float v) {
@@ -68,49 +71,57 @@ __device__ __forceinline__ bf16x8_t op8(uint32_t a, uint32_t b, uint32_t c, uint
   return __builtin_bit_cast(bf16x8_t, make_uint4(a, b, c, d));
 }
 
-// What a row tile sees, from the step's arrays; the same in every kernel.
-struct AttnRange {
+// A sequence as its rows see it, from the step's arrays.
+struct AttnSeq {
   int r0, rows;                   // first token row, query rows (tokens * G)
-  int start;                      // position of the sequence's first new token
-  int q_first, q_last;            // positions of the tile's first and last token
-  int lo, hi;                     // positions any of its rows may see, lo on a round's border
+  int start;                      // position of its first new token
+  int lo, hi;                     // positions that any row may see, lo on a round's border
+  int mts, units;                 // row tiles; rounds per tile and head (at least one: it writes the result)
 };
 
-__device__ __forceinline__ AttnRange attn_range(const KvAttnArgs &a, int b, int row0, int M) {
+__device__ __forceinline__ AttnSeq attn_seq(const KvAttnArgs &a, int b, int M, int round) {
   const KvView &kv = a.kv;
-  AttnRange x;
+  AttnSeq x;
   const int o0 = kv.offsets[b], o1 = kv.offsets[b + 1], len = kv.lens[b];
   const int e = min(max(o1, 0), kv.n_tokens);
   x.r0 = min(max(o0, 0), e);
   const int n = e - x.r0;
   x.rows = n * a.G;
   x.start = len - n;
-  const int last = min(row0 + M, x.rows) - 1;
-  x.q_first = x.start + row0 / a.G;
-  x.q_last = x.start + (last < 0 ? 0 : last / a.G);
-  const int64_t cap = (int64_t)kv.max_pages << kv.page_shift;
-  x.hi = (int)min((int64_t)x.q_last + 1, cap);
-  x.lo = a.window > 0 ? max(0, x.q_first - a.window + 1) & ~(kAttnRound - 1) : 0;
-  if (row0 >= x.rows) x.hi = x.lo;
+  x.hi = (int)min((int64_t)len, (int64_t)kv.max_pages << kv.page_shift);
+  x.lo = a.window > 0 ? max(0, x.start - a.window + 1) & ~(round - 1) : 0;
+  x.mts = min((x.rows + M - 1) / M, a.n_mt);
+  x.units = x.hi > x.lo ? (x.hi - x.lo + round - 1) / round : 1;
   return x;
 }
 
-// One wave's 32 positions: raw codes and scales in registers.
+__device__ __forceinline__ int64_t attn_units(const KvAttnArgs &a, int b, int M, int round) {
+  const AttnSeq x = attn_seq(a, b, M, round);
+  return (int64_t)x.mts * a.kv.H * x.units;
+}
+
+// One wave's 32 positions: raw codes and scales in registers. The scales of
+// positions 8g..8g+7 lie in lane group g's own row of 16 lanes, read there
+// with a row broadcast where they are used.
 template <int FMT, int D>
 struct AttnTile {
   static constexpr bool MX = FMT == GNF4_MXFP4;
   static constexpr int KW = D / 32;                          // code dwords per lane and K tile
   static constexpr int VW = MX ? (D == 256 ? 2 : 1) : D / 64;  // code pieces per lane and position
-  static constexpr int SW = MX ? (D == 256 ? 4 : D / 64) : D / 8 / 4;  // 16-byte pieces of 8 positions' scales
+  static constexpr int SW = MX ? (D == 256 ? 2 : 1) : (D == 256 ? 2 : 1);
   uint32_t kc[2][KW];
-  uint32_t ks[2];                                            // MXFP4: the lane's scale byte(s)
+  uint32_t ks[2];                 // MXFP4: scale byte(s) of the lane's K rows; NF4: words of absmax
   uint32_t vc[8][VW];
-  uint4 ksv[MX ? 1 : SW];                                    // NF4: absmax of positions 8g..8g+7
-  uint4 vsv[SW];
-  bool bad;                                                  // positions 8g..8g+7 lie on no page
+  uint32_t vs[SW];                // MXFP4: scale bytes of position 8g + c % 8; NF4: words of absmax
+  bool bad;                       // positions 8g..8g+7 lie on no page
 };
 
-template <int FMT, int D>
+// Lane N of the lane's row of 16.
+template <int N>
+__device__ __forceinline__ uint32_t row_bcast(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x150 + N, 0xf, 0xf, false);
+}
+
 __device__ __forceinline__ int attn_page(const KvView &kv, int b, int pos) {
   return kv.pages[(int64_t)b * kv.max_pages + min(pos >> kv.page_shift, kv.max_pages - 1)];
 }
@@ -120,11 +131,10 @@ struct AttnPages {
   int k, v;
 };
 
-template <int FMT, int D>
 __device__ __forceinline__ AttnPages attn_pages(const KvView &kv, int b, int t, int lane) {
   AttnPages p;
-  p.k = attn_page<FMT, D>(kv, b, t + ((lane & 15) >> 2) * 8);
-  p.v = attn_page<FMT, D>(kv, b, t + (lane >> 4) * 8);
+  p.k = attn_page(kv, b, t + ((lane & 15) >> 2) * 8);
+  p.v = attn_page(kv, b, t + (lane >> 4) * 8);
   return p;
 }
 
@@ -163,9 +173,14 @@ __device__ __forceinline__ void attn_load(AttnTile<FMT, D> &x, const KvView &kv,
       else if constexpr (D == 128) x.ks[i] = sc[g];
       else x.ks[i] = *reinterpret_cast<const uint16_t *>(sc + 2 * g);
     }
-    const uint4 *vs = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(kv.v_scales) + vrow * (D / 32));
-#pragma unroll
-    for (int w = 0; w < T::SW; ++w) x.vsv[w] = vs[w];
+    const uint8_t *sv = static_cast<const uint8_t *>(kv.v_scales) + (vrow + (r & 7)) * (D / 32);
+    if constexpr (D == 64) x.vs[0] = *reinterpret_cast<const uint16_t *>(sv);
+    else if constexpr (D == 128) x.vs[0] = *reinterpret_cast<const uint32_t *>(sv);
+    else {
+      const uint2 v = *reinterpret_cast<const uint2 *>(sv);
+      x.vs[0] = v.x;
+      x.vs[1] = v.y;
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const uint8_t *s = vp + j * (D / 2) + r * (D / 32);
@@ -188,13 +203,17 @@ __device__ __forceinline__ void attn_load(AttnTile<FMT, D> &x, const KvView &kv,
         x.kc[i][2 * b] = v.x;
         x.kc[i][2 * b + 1] = v.y;
       }
-    const int64_t srow = (((int64_t)pv * kv.H + h) << kv.page_shift) + (vt & mask);
-    const uint4 *ks = reinterpret_cast<const uint4 *>(static_cast<const float *>(kv.k_scales) + srow * (D / 64));
-    const uint4 *vs = reinterpret_cast<const uint4 *>(static_cast<const float *>(kv.v_scales) + srow * (D / 64));
-#pragma unroll
-    for (int w = 0; w < T::SW; ++w) {
-      x.ksv[w] = ks[w];
-      x.vsv[w] = vs[w];
+    // absmax of positions 8g..8g+7: D/8 words, word w in lane w % 16 of the row
+    // (D = 64: lanes 8..15 repeat lanes 0..7)
+    const int w = D == 64 ? r & 7 : r;
+    const int64_t krow8 = (((int64_t)pv * kv.H + h) << kv.page_shift) + (vt & mask);
+    const uint32_t *ks = static_cast<const uint32_t *>(kv.k_scales) + krow8 * (D / 64) + w;
+    const uint32_t *vs = static_cast<const uint32_t *>(kv.v_scales) + vrow * (D / 64) + w;
+    x.ks[0] = ks[0];
+    x.vs[0] = vs[0];
+    if constexpr (D == 256) {
+      x.ks[1] = ks[16];
+      x.vs[1] = vs[16];
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -204,11 +223,34 @@ __device__ __forceinline__ void attn_load(AttnTile<FMT, D> &x, const KvView &kv,
   }
 }
 
-// Word w of an array of 16-byte pieces (indices are compile-time constants).
-template <int N>
-__device__ __forceinline__ uint32_t word_of(const uint4 (&v)[N], int w) {
-  const uint4 &x = v[w >> 2];
-  return (w & 3) == 0 ? x.x : (w & 3) == 1 ? x.y : (w & 3) == 2 ? x.z : x.w;
+// NF4: the absmax of position 8g + J, block B of the lane's group, over the
+// operand codebook's scale.
+template <int D, int J, int B>
+__device__ __forceinline__ float nf4_absmax(const uint32_t *w) {
+  constexpr int at = J * (D / 64) + B;
+  return __builtin_bit_cast(float, row_bcast<at % 16>(w[at / 16])) * kNF4InvScale;
+}
+
+// MXFP4: scale of position 8g + J for the lane's V values (block c / (512/D)),
+// as a float32 whose exponent is the e8m0 byte (v_cvt_scalef32 reads the
+// exponent only: 0 is 2^-127, 255 gives NaN).
+template <int D, int J>
+__device__ __forceinline__ uint32_t mx_vbyte(const uint32_t *w, int c) {
+  const int blk = c / (512 / D);
+  uint32_t x = row_bcast<J>(w[0]);
+  if constexpr (D == 256) {
+    const uint32_t y = row_bcast<J>(w[1]);                   // by every lane: the source lane must be active
+    x = blk < 4 ? x : y;
+  }
+  return (x >> ((blk & 3) * 8)) & 0xffu;
+}
+
+template <int I, int N, class F>
+__device__ __forceinline__ void static_for(F &&f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    static_for<I + 1, N>(f);
+  }
 }
 
 // Copies of the NF4 byte table: one per lane of half a wave.
@@ -221,48 +263,34 @@ __device__ __forceinline__ uint32_t nf4_lut32(const uint32_t *lut, uint32_t byte
 // NQ * 16 query rows of one wave: Q operand, running statistics, O^T.
 template <int FMT, int D, int NQ>
 struct AttnWave {
-  static constexpr bool MX = FMT == GNF4_MXFP4;
-  static constexpr bool QLDS = NQ >= 4;
   static constexpr int KS = D / 32, ND = D / 16;
-  bf16x8_t q[QLDS ? 1 : NQ][QLDS ? 1 : KS];
+  bf16x8_t q[NQ][KS];
   f32x4_t o[NQ][ND];
   float m[NQ], l[NQ];
   int qpos[NQ];                                              // position of the lane's query row
 };
 
-// The scales of values j = 0..7 (positions 8g + j) for the lane's V values.
-template <int D>
-__device__ __forceinline__ uint32_t mx_vscale(const AttnTile<GNF4_MXFP4, D> &x, int j, int c) {
-  // position j's D/32 scale bytes start at byte j * D/32 of vsv
-  if constexpr (D == 64) return (word_of(x.vsv, j >> 1) >> ((j & 1) * 16 + ((c >> 3) << 3))) & 0xffu;
-  else if constexpr (D == 128) return (word_of(x.vsv, j) >> ((c >> 2) << 3)) & 0xffu;
-  else {
-    const uint32_t w = (c >> 1) < 4 ? word_of(x.vsv, 2 * j) : word_of(x.vsv, 2 * j + 1);
-    return (w >> (((c >> 1) & 3) << 3)) & 0xffu;
-  }
-}
+__device__ __forceinline__ float e8m0_scale(uint32_t byte) { return __builtin_bit_cast(float, byte << 23); }
 
 template <int FMT, int D, int NQ, bool MASKED>
 __device__ __forceinline__ void attn_tile(AttnWave<FMT, D, NQ> &w, AttnTile<FMT, D> &x, const KvAttnArgs &a,
-                                          const uint32_t *lut, const uint4 *qlds, int t, int lane) {
+                                          const uint32_t *lut, int t, int lane) {
   constexpr bool MX = FMT == GNF4_MXFP4;
   constexpr int KS = D / 32, ND = D / 16;
   const int c = lane & 15, g = lane >> 4;
   float s[NQ][8];
   // ---- scores of positions 8g..8g+7 for the lane's query row
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    f32x4_t acc[NQ];
-    f32x4_t blk[NQ];
+  static_for<0, 2>([&](auto I) {
+    constexpr int i = I;
+    f32x4_t acc[NQ], blk[NQ];
 #pragma unroll
     for (int n = 0; n < NQ; ++n) acc[n] = blk[n] = f32x4_t{0, 0, 0, 0};
-#pragma unroll
-    for (int k = 0; k < KS; ++k) {
+    static_for<0, KS>([&](auto K) {
+      constexpr int k = K;
       bf16x8_t ka;
       const uint32_t kw = x.kc[i][k];
       if constexpr (MX) {
-        const uint32_t sb = D == 256 ? (k < KS / 2 ? x.ks[i] & 0xffu : x.ks[i] >> 8) : x.ks[i];
-        const float sc = e8m0_to_f32(sb);
+        const float sc = e8m0_scale(D == 256 ? (k < KS / 2 ? x.ks[i] & 0xffu : x.ks[i] >> 8) : x.ks[i]);
         ka = op8(fp4_pair<0>(kw, sc), fp4_pair<1>(kw, sc), fp4_pair<2>(kw, sc), fp4_pair<3>(kw, sc));
       } else {
         ka = op8(nf4_lut32(lut, kw & 0xffu, lane), nf4_lut32(lut, (kw >> 8) & 0xffu, lane),
@@ -270,30 +298,25 @@ __device__ __forceinline__ void attn_tile(AttnWave<FMT, D, NQ> &w, AttnTile<FMT,
       }
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
-        bf16x8_t qv;
-        if constexpr (AttnWave<FMT, D, NQ>::QLDS) qv = __builtin_bit_cast(bf16x8_t, qlds[(n * KS + k) * 64 + lane]);
-        else qv = w.q[n][k];
-        if constexpr (MX) acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ka, qv, acc[n], 0, 0, 0);
-        else blk[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ka, qv, blk[n], 0, 0, 0);
+        if constexpr (MX) acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ka, w.q[n][k], acc[n], 0, 0, 0);
+        else blk[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ka, w.q[n][k], blk[n], 0, 0, 0);
       }
-      if constexpr (!MX) {
-        if (k & 1) {                                         // a block of 64 is complete
+      if constexpr (!MX && (k & 1)) {                        // a block of 64 is complete
+        static_for<0, 4>([&](auto J) {
+          constexpr int j = J;
+          const float ab = nf4_absmax<D, 4 * i + j, k / 2>(x.ks);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float ab = __builtin_bit_cast(float, word_of(x.ksv, (4 * i + j) * (D / 64) + k / 2)) * kNF4InvScale;
+          for (int n = 0; n < NQ; ++n) acc[n][j] = fmaf(blk[n][j], ab, acc[n][j]);
+        });
 #pragma unroll
-            for (int n = 0; n < NQ; ++n) acc[n][j] = fmaf(blk[n][j], ab, acc[n][j]);
-          }
-#pragma unroll
-          for (int n = 0; n < NQ; ++n) blk[n] = f32x4_t{0, 0, 0, 0};
-        }
+        for (int n = 0; n < NQ; ++n) blk[n] = f32x4_t{0, 0, 0, 0};
       }
-    }
+    });
 #pragma unroll
     for (int n = 0; n < NQ; ++n)
 #pragma unroll
       for (int j = 0; j < 4; ++j) s[n][4 * i + j] = acc[n][j] * a.scale_log2;
-  }
+  });
   // ---- mask, running maximum, probabilities
   uint32_t see[NQ];
   bf16x8_t pb[MX ? NQ : 1];
@@ -313,19 +336,26 @@ __device__ __forceinline__ void attn_tile(AttnWave<FMT, D, NQ> &w, AttnTile<FMT,
     float mx = s[n][0];
 #pragma unroll
     for (int j = 1; j < 8; ++j) mx = fmaxf(mx, s[n][j]);
-    mx = fmaxf(max_xor16_32(mx), w.m[n]);
-    const float ms = mx == kNegInf ? 0.0f : mx;              // nothing seen yet: exp2(-inf - 0) = 0
-    const float alpha = __builtin_amdgcn_exp2f(w.m[n] - ms);
-    w.m[n] = mx;
+    mx = max_xor16_32(mx);
+    // m is raised only when it has fallen 2^8 behind: until then the
+    // probabilities are up to 256 instead of 1, which costs no accuracy in
+    // float32 or bf16, and the sums need not be rescaled.
+    if (__any(mx > w.m[n] + 8.0f)) {
+      mx = fmaxf(mx, w.m[n]);
+      const float alpha = __builtin_amdgcn_exp2f(w.m[n] - (mx == kNegInf ? 0.0f : mx));
+      w.m[n] = mx;
+      w.l[n] *= alpha;
+#pragma unroll
+      for (int d = 0; d < ND; ++d) w.o[n][d] *= alpha;
+    }
+    const float ms = w.m[n] == kNegInf ? 0.0f : w.m[n];      // nothing seen yet: exp2(-inf - 0) = 0
     float sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       s[n][j] = __builtin_amdgcn_exp2f(s[n][j] - ms);
       sum += s[n][j];
     }
-    w.l[n] = w.l[n] * alpha + sum;
-#pragma unroll
-    for (int d = 0; d < ND; ++d) w.o[n][d] *= alpha;
+    w.l[n] += sum;
     if constexpr (MX)
       pb[n] = op8(pk_bf16(s[n][0], s[n][1]), pk_bf16(s[n][2], s[n][3]), pk_bf16(s[n][4], s[n][5]),
                   pk_bf16(s[n][6], s[n][7]));
@@ -333,8 +363,7 @@ __device__ __forceinline__ void attn_tile(AttnWave<FMT, D, NQ> &w, AttnTile<FMT,
   // ---- O^T += V^T P^T
   if constexpr (MX) {
     uint32_t sb[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sb[j] = mx_vscale<D>(x, j, c);
+    static_for<0, 8>([&](auto J) { sb[J] = mx_vbyte<D, J>(x.vs, c); });
     if constexpr (MASKED) {
       // A NaN scale in a place that some row does not see: 0 * NaN must not
       // reach that row. Such values are taken out of the product and their NaN
@@ -365,7 +394,7 @@ __device__ __forceinline__ void attn_tile(AttnWave<FMT, D, NQ> &w, AttnTile<FMT,
     }
     float sc[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sc[j] = e8m0_to_f32(sb[j]);
+    for (int j = 0; j < 8; ++j) sc[j] = e8m0_scale(sb[j]);
     // byte y of a lane's codes holds its values 2y and 2y+1
 #pragma unroll
     for (int y = 0; y < ND / 2; ++y) {
@@ -391,12 +420,10 @@ __device__ __forceinline__ void attn_tile(AttnWave<FMT, D, NQ> &w, AttnTile<FMT,
     }
   } else {
     // the absmax of (position, block) goes into the probabilities of that block
-#pragma unroll
-    for (int b = 0; b < D / 64; ++b) {
+    static_for<0, D / 64>([&](auto BL) {
+      constexpr int b = BL;
       float ab[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        ab[j] = __builtin_bit_cast(float, word_of(x.vsv, j * (D / 64) + b)) * kNF4InvScale;
+      static_for<0, 8>([&](auto J) { ab[J] = nf4_absmax<D, J, b>(x.vs); });
       bf16x8_t pq[NQ];
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
@@ -427,7 +454,7 @@ __device__ __forceinline__ void attn_tile(AttnWave<FMT, D, NQ> &w, AttnTile<FMT,
           w.o[n][d + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, pq[n], w.o[n][d + 1], 0, 0, 0);
         }
       }
-    }
+    });
   }
 }
 
@@ -454,255 +481,359 @@ __device__ __forceinline__ AttnScale attn_finish(float m, float l, const float *
   return r;
 }
 
-template <int FMT, int D, int NQ>
-__global__ __launch_bounds__(kAttnThreads, 2) void kv_attn_kernel(KvAttnArgs a) {
+// Shares of the numbered rounds: workgroup w takes [w * share, (w + 1) * share).
+__device__ __forceinline__ int64_t attn_share(int64_t total) { return (total + kAttnGroups - 1) / kAttnGroups; }
+
+// Sum over the workgroup of one value per thread, in every thread.
+__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t *lds, int tid, int waves) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
+  __syncthreads();
+  if ((tid & 63) == 0) lds[tid >> 6] = v;
+  __syncthreads();
+  v = 0;
+  for (int i = 0; i < waves; ++i) v += lds[i];
+  return v;
+}
+
+template <int FMT, int D, int NQ, int NW>
+__global__ __launch_bounds__(64 * NW, NW / 4) void kv_attn_kernel(KvAttnArgs a) {
   constexpr bool MX = FMT == GNF4_MXFP4;
+  constexpr int NT = 64 * NW, ROUND = 32 * NW;
   constexpr int KS = D / 32, ND = D / 16, M = 16 * NQ;
-  constexpr bool QLDS = AttnWave<FMT, D, NQ>::QLDS;
-  constexpr int RED = 4 * 16 * (D + 4);                      // words: the four waves' O tile
+  constexpr int DC = D < 128 ? D : 128;                      // values of a row joined at a time
   constexpr int LUT = MX ? 0 : 256 * kAttnLutCopies;
-  constexpr int QW = QLDS ? NQ * KS * 64 * 4 : 0;
-  constexpr int WORDS = (LUT + QW) > RED ? (LUT + QW) : RED;
-  __shared__ __attribute__((aligned(16))) uint32_t lds[WORDS];
-  __shared__ float sm[4][NQ * 16], sl[4][NQ * 16];
-  uint32_t *lut = lds;
-  uint4 *qlds = reinterpret_cast<uint4 *>(lds + LUT);
+  constexpr int DEPTH = D == 256 || NQ > 1 ? 2 : 3;          // tiles in registers: one computed, the others in flight
+  __shared__ __attribute__((aligned(16))) uint32_t lut[LUT ? LUT : 4];
+  __shared__ __attribute__((aligned(16))) float red[NW * 16 * (DC + 4)];
+  __shared__ float sm[NW][M], sl[NW][M];
+  __shared__ int64_t pre[NT + 1];
+  __shared__ int64_t wsum[NW];
   const KvView &kv = a.kv;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = lane & 15, g = lane >> 4;
-  // heads fastest, then row tiles (the last tiles see the most), sequences, splits
-  int idx = (int)blockIdx.x;
-  const int h = idx % kv.H;
-  idx /= kv.H;
-  const int mt = a.n_mt - 1 - idx % a.n_mt;
-  idx /= a.n_mt;
-  const int b = idx % kv.B, split = idx / kv.B;
-  const int row0 = mt * M, Hq = kv.H * a.G;
-  const AttnRange x = attn_range(a, b, row0, M);
-  if (row0 >= x.rows) return;
-  const int t0 = x.lo + split * a.chunk;
-  const int t1 = split == a.n_split - 1 ? x.hi : min(x.hi, t0 + a.chunk);
-  if (t0 >= t1 && split > 0) return;
-  const bool whole = split == 0 && t1 >= x.hi;               // the only range of this tile
-
-  AttnWave<FMT, D, NQ> w;
-#pragma unroll
-  for (int n = 0; n < NQ; ++n) {
-    const int row = row0 + n * 16 + c, tok = row / a.G;
-    const bool ok = row < x.rows;
-    w.qpos[n] = ok ? x.start + tok : -1;
-    w.m[n] = kNegInf;
-    w.l[n] = 0.0f;
-    const uint16_t *qp = a.q + (int64_t)(x.r0 + tok) * a.q_stride + (int64_t)(h * a.G + row - tok * a.G) * D;
-#pragma unroll
-    for (int k = 0; k < KS; ++k) {
-      const int d = MX ? g * (D / 4) + k * 8 : (k >> 1) * 64 + g * 16 + (k & 1) * 8;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (ok && (!QLDS || wave == n)) v = *reinterpret_cast<const uint4 *>(qp + d);
-      if constexpr (QLDS) {
-        if (wave == n) qlds[(n * KS + k) * 64 + lane] = v;
-      } else {
-        w.q[n][k] = __builtin_bit_cast(bf16x8_t, v);
-      }
-    }
-#pragma unroll
-    for (int d = 0; d < ND; ++d) w.o[n][d] = f32x4_t{0, 0, 0, 0};
-  }
+  const int Hq = kv.H * a.G;
   if constexpr (!MX) {
     // entry b, copies 4j..4j+3 as one 16-byte store
 #pragma unroll 4
-    for (int i = tid; i < 256 * kAttnLutCopies / 4; i += kAttnThreads) {
+    for (int i = tid; i < 256 * kAttnLutCopies / 4; i += NT) {
       const uint32_t e = (uint32_t)i / (kAttnLutCopies / 4);
       const uint32_t v = nf4_bf16(e >> 4) | (nf4_bf16(e & 15u) << 16);
       *reinterpret_cast<uint4 *>(lut + 4 * i) = make_uint4(v, v, v, v);
     }
-  }
-  if constexpr (!MX || QLDS) __syncthreads();
-
-  const int full_lo = a.window > 0 ? x.q_last - a.window + 1 : 0;   // seen by every row from here ...
-  const int full_hi = x.q_first;                                    // ... up to here
-  // One round ahead the codes are in flight, two rounds ahead the page ids.
-  AttnTile<FMT, D> ta, tb;
-  int t = t0 + wave * 32;
-  auto tile = [&](AttnTile<FMT, D> &cur, int at) {
-    const bool all = at >= full_lo && at + 31 <= full_hi && __ballot(cur.bad) == 0;
-    if (all) attn_tile<FMT, D, NQ, false>(w, cur, a, lut, qlds, at, lane);
-    else attn_tile<FMT, D, NQ, true>(w, cur, a, lut, qlds, at, lane);
-  };
-  if (t < t1) {
-    AttnPages p = attn_pages<FMT, D>(kv, b, t, lane);
-    AttnPages pn = attn_pages<FMT, D>(kv, b, t + kAttnRound, lane);
-    attn_load<FMT, D>(ta, kv, h, t, p, lane);
-    for (;;) {
-      p = attn_pages<FMT, D>(kv, b, t + 2 * kAttnRound, lane);
-      if (t + kAttnRound < t1) attn_load<FMT, D>(tb, kv, h, t + kAttnRound, pn, lane);
-      tile(ta, t);
-      t += kAttnRound;
-      if (t >= t1) break;
-      pn = attn_pages<FMT, D>(kv, b, t + 2 * kAttnRound, lane);
-      if (t + kAttnRound < t1) attn_load<FMT, D>(ta, kv, h, t + kAttnRound, p, lane);
-      tile(tb, t);
-      t += kAttnRound;
-      if (t >= t1) break;
-    }
+    __syncthreads();
   }
 
-  // ---- join the four waves
+  // ---- the run of rounds: [u, end), from sequence b0 + (an index into pre) on
+  int64_t u = 0, end = 0, base = 0;                          // base: rounds before the sequences of pre
+  int b = 0, b0 = 0;
+  if (a.shared) {
+    int64_t v = tid < kv.B ? attn_units(a, tid, M, ROUND) : 0, total = v;
+    for (int i = tid + NT; i < kv.B; i += NT) total += attn_units(a, i, M, ROUND);
+    total = block_sum(total, wsum, tid, NW);
+    const int64_t share = attn_share(total);
+    u = blockIdx.x * share;
+    end = min(total, u + share);
+    if (u >= end) return;
+    for (;;) {                                               // the chunk of sequences that holds round u
+      int64_t s = v;
 #pragma unroll
-  for (int n = 0; n < NQ; ++n) {
-    w.l[n] = sum_xor16_32(w.l[n]);
-    if (g == 0) {
-      sm[wave][n * 16 + c] = w.m[n];
-      sl[wave][n * 16 + c] = w.l[n];
+      for (int d = 1; d < 64; d <<= 1) {
+        const int64_t o = __shfl_up(s, d, 64);
+        if (lane >= d) s += o;
+      }
+      __syncthreads();
+      if (lane == 63) wsum[wave] = s;
+      __syncthreads();
+      int64_t before = base;
+      for (int i = 0; i < wave; ++i) before += wsum[i];
+      pre[tid + 1] = before + s;
+      if (tid == 0) pre[0] = base;
+      __syncthreads();
+      if (u < pre[NT] || b0 + NT >= kv.B) break;
+      base = pre[NT];
+      b0 += NT;
+      v = b0 + tid < kv.B ? attn_units(a, b0 + tid, M, ROUND) : 0;
+    }
+    for (int lo = 0, n = NT; n > 1;) {             // the last sequence with pre <= u: 64 probes at a time
+      const int step = (n + 63) >> 6;
+      const bool below = lane * step < n && pre[lo + lane * step] <= u;
+      const int k = __popcll(__ballot(below));
+      lo += (k - 1) * step;
+      n = min(step, n - (k - 1) * step);
+      b = lo;
     }
   }
-  __syncthreads();
-  float *red = reinterpret_cast<float *>(lds);
-  const int64_t item = ((int64_t)b * a.n_mt + mt) * kv.H + h;
+
+  for (;;) {
+    // ---- the next problem: tile mt, head h of sequence bb; its rounds [q0, q1)
+    int bb, mt, h, q0 = 0, q1;
+    AttnSeq x;
+    if (a.shared) {
+      if (u >= end) return;
+      while (u >= pre[b + 1]) {                              // sequences without rows have no rounds
+        if (++b < NT) continue;
+        base = pre[NT];
+        b0 += NT;
+        b = 0;
+        int64_t s = b0 + tid < kv.B ? attn_units(a, b0 + tid, M, ROUND) : 0;
 #pragma unroll
-  for (int n = 0; n < NQ; ++n) {
-    const int r = n * 16 + c;
-    const float top = fmaxf(fmaxf(sm[0][r], sm[1][r]), fmaxf(sm[2][r], sm[3][r]));
-    const float ts = top == kNegInf ? 0.0f : top;
-    const float f = __builtin_amdgcn_exp2f(w.m[n] - ts);
-    float *mine = red + (wave * 16 + c) * (D + 4);
-#pragma unroll
-    for (int d = 0; d < ND; ++d)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int cc = g * 4 + i;
-        const int at = MX ? cc * (D / 16) + d : (d >> 2) * 64 + cc * 4 + (d & 3);
-        mine[at] = w.o[n][d][i] * f;
-      }
-    __syncthreads();
-    // 16 rows x D/4 groups of four values over the workgroup
-    for (int u = tid; u < 16 * (D / 4); u += kAttnThreads) {
-      const int rr = u / (D / 4), d4 = (u - rr * (D / 4)) * 4;
-      const int row = row0 + n * 16 + rr;
-      if (row < x.rows) {
-        float4 s = make_float4(0, 0, 0, 0);
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const float4 o = *reinterpret_cast<const float4 *>(red + (v * 16 + rr) * (D + 4) + d4);
-          s.x += o.x;
-          s.y += o.y;
-          s.z += o.z;
-          s.w += o.w;
+        for (int d = 1; d < 64; d <<= 1) {
+          const int64_t o = __shfl_up(s, d, 64);
+          if (lane >= d) s += o;
         }
-        const int k = n * 16 + rr;
-        const float mr = fmaxf(fmaxf(sm[0][k], sm[1][k]), fmaxf(sm[2][k], sm[3][k]));
-        const float mrs = mr == kNegInf ? 0.0f : mr;
-        float l = 0.0f;
+        __syncthreads();
+        if (lane == 63) wsum[wave] = s;
+        __syncthreads();
+        int64_t before = base;
+        for (int i = 0; i < wave; ++i) before += wsum[i];
+        pre[tid + 1] = before + s;
+        if (tid == 0) pre[0] = base;
+        __syncthreads();
+      }
+      bb = b0 + b;
+      x = attn_seq(a, bb, M, ROUND);
+      const int64_t rel = u - pre[b], item = rel / x.units;
+      q0 = (int)(rel - item * x.units);
+      mt = (int)(item / kv.H);
+      h = (int)(item - (int64_t)mt * kv.H);
+      q1 = (int)min((int64_t)x.units, q0 + (end - u));
+      u += q1 - q0;
+    } else {
+      int idx = (int)blockIdx.x;
+      h = idx % kv.H;
+      idx /= kv.H;
+      mt = idx % a.n_mt;
+      bb = idx / a.n_mt;
+      x = attn_seq(a, bb, M, ROUND);
+      if (mt >= x.mts) return;
+      q1 = x.units;
+    }
+    const bool whole = q0 == 0 && q1 == x.units;
+    const int t0 = x.lo + q0 * ROUND, t1 = min(x.hi, x.lo + q1 * ROUND), row0 = mt * M;
+
+    AttnWave<FMT, D, NQ> w;
 #pragma unroll
-        for (int v = 0; v < 4; ++v) l += sl[v][k] * __builtin_amdgcn_exp2f(sm[v][k] - mrs);
-        if (whole) {
-          const int tok = row / a.G, hq = h * a.G + row - tok * a.G;
-          const AttnScale z = attn_finish(mr, l, a.sinks, hq);
-          *reinterpret_cast<uint2 *>(a.out + (int64_t)(x.r0 + tok) * a.out_stride + (int64_t)hq * D + d4) =
-              make_uint2(pk_bf16(s.x * z.mul, s.y * z.mul), pk_bf16(s.z * z.mul, s.w * z.mul));
-          if (a.lse && d4 == 0) a.lse[(int64_t)(x.r0 + tok) * Hq + hq] = z.lse;
-        } else {
-          const int64_t pr = (item * a.n_split + split) * M + k;
-          *reinterpret_cast<float4 *>(a.part + pr * D + d4) = s;
-          if (d4 == 0) *reinterpret_cast<float2 *>(a.part + a.part_rows * D + pr * 2) = make_float2(mr, l);
+    for (int n = 0; n < NQ; ++n) {
+      const int row = row0 + n * 16 + c, tok = row / a.G;
+      const bool ok = row < x.rows;
+      w.qpos[n] = ok ? x.start + tok : -1;
+      w.m[n] = kNegInf;
+      w.l[n] = 0.0f;
+      const uint16_t *qp = a.q + (int64_t)(x.r0 + tok) * a.q_stride + (int64_t)(h * a.G + row - tok * a.G) * D;
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        const int d = MX ? g * (D / 4) + k * 8 : (k >> 1) * 64 + g * 16 + (k & 1) * 8;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (ok) v = *reinterpret_cast<const uint4 *>(qp + d);
+        w.q[n][k] = __builtin_bit_cast(bf16x8_t, v);
+      }
+#pragma unroll
+      for (int d = 0; d < ND; ++d) w.o[n][d] = f32x4_t{0, 0, 0, 0};
+    }
+    const int last = min(row0 + M, x.rows) - 1;
+    const int full_hi = x.start + row0 / a.G;                // every row sees from full_lo to full_hi
+    const int full_lo = a.window > 0 ? x.start + last / a.G - a.window + 1 : 0;
+    AttnTile<FMT, D> tl[DEPTH];
+    AttnPages pg[DEPTH];
+    int t = t0 + wave * 32;
+    if (t < t1) {
+      // DEPTH - 1 rounds ahead the codes are in flight, one more the page ids
+#pragma unroll
+      for (int i = 0; i < DEPTH; ++i) pg[i] = attn_pages(kv, bb, t + i * ROUND, lane);
+#pragma unroll
+      for (int i = 0; i < DEPTH - 1; ++i)
+        if (t + i * ROUND < t1) attn_load<FMT, D>(tl[i], kv, h, t + i * ROUND, pg[i], lane);
+      for (bool more = true; more;) {
+#pragma unroll
+        for (int i = 0; i < DEPTH; ++i) {
+          constexpr int A = DEPTH - 1;
+          pg[i] = attn_pages(kv, bb, t + DEPTH * ROUND, lane);
+          if (t + A * ROUND < t1)
+            attn_load<FMT, D>(tl[(i + A) % DEPTH], kv, h, t + A * ROUND, pg[(i + A) % DEPTH], lane);
+          const bool all = t >= full_lo && t + 31 <= full_hi && __ballot(tl[i].bad) == 0;
+          if (all) attn_tile<FMT, D, NQ, false>(w, tl[i], a, lut, t, lane);
+          else attn_tile<FMT, D, NQ, true>(w, tl[i], a, lut, t, lane);
+          t += ROUND;
+          if (t >= t1) {
+            more = false;
+            break;
+          }
         }
       }
     }
+
+    // ---- join the waves
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      w.l[n] = sum_xor16_32(w.l[n]);
+      if (g == 0) {
+        sm[wave][n * 16 + c] = w.m[n];
+        sl[wave][n * 16 + c] = w.l[n];
+      }
+    }
     __syncthreads();
+    // a problem that goes on from the workgroup before lies in this one's first
+    // slot, one that goes on in the next in its second
+    const int64_t slot = 2 * (int64_t)blockIdx.x + (q0 == 0 ? 1 : 0);
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      const int r = n * 16 + c;
+      float top = sm[0][r];
+#pragma unroll
+      for (int v = 1; v < NW; ++v) top = fmaxf(top, sm[v][r]);
+      const float f = __builtin_amdgcn_exp2f(w.m[n] - (top == kNegInf ? 0.0f : top));
+#pragma unroll
+      for (int dc = 0; dc < D; dc += DC) {
+        float *mine = red + (wave * 16 + c) * (DC + 4);
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int cc = g * 4 + i;
+            const int at = MX ? cc * (D / 16) + d : (d >> 2) * 64 + cc * 4 + (d & 3);
+            if (at >= dc && at < dc + DC) mine[at - dc] = w.o[n][d][i] * f;
+          }
+        __syncthreads();
+        for (int k4 = tid; k4 < 16 * (DC / 4); k4 += NT) {
+          const int rr = k4 / (DC / 4), d4 = (k4 - rr * (DC / 4)) * 4;
+          const int k = n * 16 + rr, row = row0 + k;
+          if (row < x.rows) {
+            float4 s = make_float4(0, 0, 0, 0);
+            float mr = sm[0][k], l = 0.0f;
+#pragma unroll
+            for (int v = 0; v < NW; ++v) {
+              const float4 o = *reinterpret_cast<const float4 *>(red + (v * 16 + rr) * (DC + 4) + d4);
+              s.x += o.x;
+              s.y += o.y;
+              s.z += o.z;
+              s.w += o.w;
+              mr = fmaxf(mr, sm[v][k]);
+            }
+            const float mrs = mr == kNegInf ? 0.0f : mr;
+#pragma unroll
+            for (int v = 0; v < NW; ++v) l += sl[v][k] * __builtin_amdgcn_exp2f(sm[v][k] - mrs);
+            if (whole) {
+              const int tok = row / a.G, hq = h * a.G + row - tok * a.G;
+              const AttnScale z = attn_finish(mr, l, a.sinks, hq);
+              *reinterpret_cast<uint2 *>(a.out + (int64_t)(x.r0 + tok) * a.out_stride + (int64_t)hq * D + dc + d4) =
+                  make_uint2(pk_bf16(s.x * z.mul, s.y * z.mul), pk_bf16(s.z * z.mul, s.w * z.mul));
+              if (a.lse && dc + d4 == 0) a.lse[(int64_t)(x.r0 + tok) * Hq + hq] = z.lse;
+            } else {
+              const int64_t pr = slot * M + k;
+              *reinterpret_cast<float4 *>(a.part + pr * D + dc + d4) = s;
+              if (dc + d4 == 0)
+                *reinterpret_cast<float2 *>(a.part + 2LL * kAttnGroups * M * D + pr * 2) = make_float2(mr, l);
+            }
+          }
+        }
+        __syncthreads();
+      }
+    }
+    if (!a.shared) return;
   }
 }
 
-// Joins the ranges of one tile: a thread per four values of a row.
+// Puts together the problems that lie in several runs: a workgroup per problem,
+// a thread per four values of a row.
+constexpr int kJoinThreads = 256;
+
 template <int D>
-__global__ __launch_bounds__(kAttnThreads) void kv_attn_join_kernel(KvAttnArgs a, int M) {
+__global__ __launch_bounds__(kJoinThreads) void kv_attn_join_kernel(KvAttnArgs a, int M, int round) {
+  __shared__ int64_t wsum[kJoinThreads / 64];
   const KvView &kv = a.kv;
+  const int tid = threadIdx.x;
   int idx = (int)blockIdx.x;
-  const int64_t item = idx;
   const int h = idx % kv.H;
   idx /= kv.H;
   const int mt = idx % a.n_mt, b = idx / a.n_mt;
-  const int u = (int)blockIdx.y * kAttnThreads + threadIdx.x;
-  const int r = u / (D / 4), d4 = (u - r * (D / 4)) * 4, row = mt * M + r;
-  const AttnRange x = attn_range(a, b, mt * M, M);
-  if (r >= M || row >= x.rows) return;
-  const int n = x.hi > x.lo ? min((x.hi - x.lo + a.chunk - 1) / a.chunk, a.n_split) : 1;
-  if (n <= 1) return;                                        // written by its only range
-  const float2 *ml = reinterpret_cast<const float2 *>(a.part + a.part_rows * D) + item * a.n_split * M + r;
-  const float *po = a.part + (item * a.n_split * M + r) * D + d4;
-  float top = kNegInf;
-#pragma unroll 8
-  for (int s = 0; s < n; ++s) top = fmaxf(top, ml[(int64_t)s * M].x);
-  const float ts = top == kNegInf ? 0.0f : top;
-  float l = 0.0f;
-  float4 o = make_float4(0, 0, 0, 0);
-#pragma unroll 8
-  for (int s = 0; s < n; ++s) {
-    const float2 v = ml[(int64_t)s * M];
-    const float4 p = *reinterpret_cast<const float4 *>(po + (int64_t)s * M * D);
-    const float f = __builtin_amdgcn_exp2f(v.x - ts);
-    l = fmaf(v.y, f, l);
-    o.x = fmaf(p.x, f, o.x);
-    o.y = fmaf(p.y, f, o.y);
-    o.z = fmaf(p.z, f, o.z);
-    o.w = fmaf(p.w, f, o.w);
+  const AttnSeq x = attn_seq(a, b, M, round);
+  int64_t first = 0, total = 0;
+  for (int i = tid; i < kv.B; i += kJoinThreads) {
+    const int64_t n = attn_units(a, i, M, round);
+    total += n;
+    first += i < b ? n : 0;
   }
-  const int tok = row / a.G, hq = h * a.G + row - tok * a.G;
-  const AttnScale z = attn_finish(top, l, a.sinks, hq);
-  *reinterpret_cast<uint2 *>(a.out + (int64_t)(x.r0 + tok) * a.out_stride + (int64_t)hq * D + d4) =
-      make_uint2(pk_bf16(o.x * z.mul, o.y * z.mul), pk_bf16(o.z * z.mul, o.w * z.mul));
-  if (a.lse && d4 == 0) a.lse[(int64_t)(x.r0 + tok) * kv.H * a.G + hq] = z.lse;
+  total = block_sum(total, wsum, tid, kJoinThreads / 64);
+  first = block_sum(first, wsum, tid, kJoinThreads / 64);
+  if (mt >= x.mts) return;
+  const int64_t share = attn_share(total);
+  first += ((int64_t)mt * kv.H + h) * x.units;
+  const int64_t w0 = first / share, w1 = (first + x.units - 1) / share;
+  if (w0 == w1) return;                                      // written by its only workgroup
+  const int n = (int)(w1 - w0) + 1;
+  const float2 *ml = reinterpret_cast<const float2 *>(a.part + 2LL * kAttnGroups * M * D);
+  for (int u = tid; u < M * (D / 4); u += kJoinThreads) {
+    const int r = u / (D / 4), d4 = (u - r * (D / 4)) * 4, row = mt * M + r;
+    if (row >= x.rows) break;
+    // the first workgroup's second slot, the first slots of the others
+    auto at = [&](int s) { return (2 * (w0 + s) + (s == 0 ? 1 : 0)) * M + r; };
+    float top = kNegInf, l = 0.0f;
+    float4 o = make_float4(0, 0, 0, 0);
+#pragma unroll 4
+    for (int s = 0; s < n; ++s) {
+      const int64_t pr = at(s);
+      const float2 v = ml[pr];
+      const float4 p = *reinterpret_cast<const float4 *>(a.part + pr * D + d4);
+      const float nt = fmaxf(top, v.x), ns = nt == kNegInf ? 0.0f : nt;
+      const float f = __builtin_amdgcn_exp2f(top - ns), e = __builtin_amdgcn_exp2f(v.x - ns);
+      top = nt;
+      l = l * f + v.y * e;
+      o.x = o.x * f + p.x * e;
+      o.y = o.y * f + p.y * e;
+      o.z = o.z * f + p.z * e;
+      o.w = o.w * f + p.w * e;
+    }
+    const int tok = row / a.G, hq = h * a.G + row - tok * a.G;
+    const AttnScale z = attn_finish(top, l, a.sinks, hq);
+    *reinterpret_cast<uint2 *>(a.out + (int64_t)(x.r0 + tok) * a.out_stride + (int64_t)hq * D + d4) =
+        make_uint2(pk_bf16(o.x * z.mul, o.y * z.mul), pk_bf16(o.z * z.mul, o.w * z.mul));
+    if (a.lse && d4 == 0) a.lse[(int64_t)(x.r0 + tok) * kv.H * a.G + hq] = z.lse;
+  }
 }
 
-// Rows per tile from the most new tokens of a sequence; enough ranges that a
-// few workgroups per compute unit exist, none shorter than two rounds.
+// Rows per tile from the most new tokens of a sequence. Short contexts, of up
+// to four rounds, take a workgroup per problem and one launch.
 bool kv_attention_plan(int32_t D, int32_t H, int32_t G, int32_t B, int64_t n_tokens, int32_t max_new,
                        int64_t max_len, int32_t window, KvAttnPlan *p) {
   const int64_t rows = (int64_t)max_new * G;
-  p->nq = rows <= 16 ? 1 : (rows <= 32 || D == 256) ? 2 : 4;
+  p->nq = rows <= 16 || D == 256 ? 1 : 2;                     // D = 256: the registers hold no second tile
+  p->waves = p->nq == 1 && D <= 128 ? 8 : 4;
+  const int round = 32 * p->waves;
   const int M = 16 * p->nq;
   const int64_t n_mt = (rows + M - 1) / M;
   p->items = (int64_t)B * n_mt * H;
-  constexpr int64_t kTarget = 1024;
-  const int64_t busy = std::min<int64_t>((int64_t)B * n_mt, (n_tokens * G) / M + B) * H;
   int64_t len = std::max<int64_t>(max_len, 1);
-  if (window > 0) len = std::min<int64_t>(len, (int64_t)window + max_new + kAttnRound);
-  int64_t split = std::min<int64_t>(std::max<int64_t>(kTarget / std::max<int64_t>(busy, 1), 1),
-                                    (len + 2 * kAttnRound - 1) / (2 * kAttnRound));
-  int64_t chunk = ((len + split - 1) / split + kAttnRound - 1) / kAttnRound * kAttnRound;
-  split = (len + chunk - 1) / chunk;
-  if (p->items * split > 0x7fffffffLL || n_mt > 0x7fffffffLL) return false;
+  if (window > 0) len = std::min<int64_t>(len, (int64_t)window + max_new - 1 + round - 1);
+  if (p->items > 0x7fffffffLL) return false;
   p->n_mt = (int32_t)n_mt;
-  p->n_split = (int32_t)split;
-  p->chunk = (int32_t)std::min<int64_t>(chunk, 0x40000000LL);
-  p->bytes = split > 1 ? (size_t)(p->items * split * M) * (D + 2) * 4 : 0;
+  p->shared = len > 4 * round;
+  p->bytes = p->shared ? (size_t)(2 * kAttnGroups * M) * (D + 2) * 4 : 0;
   return true;
 }
 
 template <int FMT, int D, int NQ>
 static hipError_t attn_go(const KvAttnArgs &a, const KvAttnPlan &p, hipStream_t s) {
-  hipLaunchKernelGGL((kv_attn_kernel<FMT, D, NQ>), dim3((unsigned)(p.items * p.n_split)), dim3(kAttnThreads), 0, s, a);
+  constexpr int NW = NQ == 1 && D <= 128 ? 8 : 4;
+  hipLaunchKernelGGL((kv_attn_kernel<FMT, D, NQ, NW>), dim3(p.shared ? kAttnGroups : (unsigned)p.items), dim3(64 * NW),
+                     0, s, a);
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || p.n_split == 1) return e;
-  const int M = 16 * NQ;
-  hipLaunchKernelGGL((kv_attn_join_kernel<D>), dim3((unsigned)p.items, (M * (D / 4) + kAttnThreads - 1) / kAttnThreads),
-                     dim3(kAttnThreads), 0, s, a, M);
+  if (e != hipSuccess || !p.shared) return e;
+  hipLaunchKernelGGL((kv_attn_join_kernel<D>), dim3((unsigned)p.items), dim3(kJoinThreads), 0, s, a, 16 * NQ, 32 * NW);
   return hipGetLastError();
 }
 
 template <int FMT, int D>
 static hipError_t attn_nq(const KvAttnArgs &a, const KvAttnPlan &p, hipStream_t s) {
-  if (p.nq == 1) return attn_go<FMT, D, 1>(a, p, s);
-  if constexpr (D != 256) {
-    if (p.nq == 4) return attn_go<FMT, D, 4>(a, p, s);
+  if constexpr (D <= 128) {
+    if (p.nq == 2) return attn_go<FMT, D, 2>(a, p, s);
   }
-  return attn_go<FMT, D, 2>(a, p, s);
+  return attn_go<FMT, D, 1>(a, p, s);
 }
 
 hipError_t launch_kv_attention(const KvAttnArgs &args, const KvAttnPlan &p, int32_t format, hipStream_t s) {
   KvAttnArgs a = args;
   a.n_mt = p.n_mt;
-  a.n_split = p.n_split;
-  a.chunk = p.chunk;
-  a.part_rows = p.items * p.n_split * 16 * p.nq;
+  a.shared = p.shared;
   if (format == GNF4_MXFP4) {
     if (a.kv.D == 64) return attn_nq<GNF4_MXFP4, 64>(a, p, s);
     if (a.kv.D == 128) return attn_nq<GNF4_MXFP4, 128>(a, p, s);

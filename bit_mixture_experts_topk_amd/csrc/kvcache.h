@@ -34,15 +34,15 @@ struct KvAttnArgs {
   int32_t G;                      // query heads per cache head
   int32_t window;                 // 0: none
   float scale_log2;               // scale * log2(e): the softmax runs in base 2
-  int32_t n_mt, n_split, chunk;   // row tiles per sequence, splits, tokens per split
-  float *part;                    // [items][n_split][M][D] then [items][n_split][M][2]
-  int64_t part_rows;              // items * n_split * M
+  int32_t n_mt;                   // most row tiles of one sequence
+  int32_t shared;                 // 1: equal shares of all work per workgroup; 0: a workgroup per tile
+  float *part;                    // [slots][M][D] then [slots][M][2], two slots per workgroup
 };
 
-// How one call is cut: rows per tile, tiles, splits (attention.hip).
+// How one call is cut (attention.hip).
 struct KvAttnPlan {
-  int32_t nq, n_mt, n_split, chunk;
-  int64_t items;
+  int32_t nq, waves, n_mt, shared;
+  int64_t items;                  // sequences * n_mt * H
   size_t bytes;
 };
 bool kv_attention_plan(int32_t D, int32_t H, int32_t G, int32_t B, int64_t n_tokens, int32_t max_new,

@@ -672,9 +672,9 @@ def _positions(positions, rope, T, dev):
 
 
 def _result(out, like, T, H, D, name, dev):
-    """(tensor, token stride) of a result [T, H, D]: the given one, or a new one."""
+    """(tensor, token stride) of a result [T, H, D]: the given one, or a new one like `like`."""
     if out is None:
-        return torch.empty((T, H, D), dtype=like.dtype, device=like.device), H * D
+        return torch.empty_like(like, memory_format=torch.contiguous_format), H * D
     return out, _heads(out, T, H, D, name, dev)
 
 
