@@ -34,6 +34,7 @@
 // D/16 values of every one of 8 positions and pairs of positions are put
 // together after decoding.
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "kvcache.h"
@@ -75,7 +76,7 @@ __device__ __forceinline__ bf16x8_t op8(uint32_t a, uint32_t b, uint32_t c, uint
 struct AttnSeq {
   int r0, rows;                   // first token row, query rows (tokens * G)
   int start;                      // position of its first new token
-  int lo, hi;                     // positions that any row may see, lo on a round's border
+  int lo, hi;                     // positions that any row may see, lo a multiple of 32
   int mts, units;                 // row tiles; rounds per tile and head (at least one: it writes the result)
 };
 
@@ -89,7 +90,7 @@ __device__ __forceinline__ AttnSeq attn_seq(const KvAttnArgs &a, int b, int M, i
   x.rows = n * a.G;
   x.start = len - n;
   x.hi = (int)min((int64_t)len, (int64_t)kv.max_pages << kv.page_shift);
-  x.lo = a.window > 0 ? max(0, x.start - a.window + 1) & ~(round - 1) : 0;
+  x.lo = a.window > 0 ? max(0, x.start - a.window + 1) & ~31 : 0;
   x.mts = min((x.rows + M - 1) / M, a.n_mt);
   x.units = x.hi > x.lo ? (x.hi - x.lo + round - 1) / round : 1;
   return x;
@@ -223,12 +224,11 @@ __device__ __forceinline__ void attn_load(AttnTile<FMT, D> &x, const KvView &kv,
   }
 }
 
-// NF4: the absmax of position 8g + J, block B of the lane's group, over the
-// operand codebook's scale.
+// NF4: the absmax of position 8g + J, block B of the lane's group.
 template <int D, int J, int B>
 __device__ __forceinline__ float nf4_absmax(const uint32_t *w) {
   constexpr int at = J * (D / 64) + B;
-  return __builtin_bit_cast(float, row_bcast<at % 16>(w[at / 16])) * kNF4InvScale;
+  return __builtin_bit_cast(float, row_bcast<at % 16>(w[at / 16]));
 }
 
 // MXFP4: scale of position 8g + J for the lane's V values (block c / (512/D)),
@@ -253,13 +253,6 @@ __device__ __forceinline__ void static_for(F &&f) {
   }
 }
 
-// Copies of the NF4 byte table: one per lane of half a wave.
-constexpr int kAttnLutCopies = 32;
-
-__device__ __forceinline__ uint32_t nf4_lut32(const uint32_t *lut, uint32_t byte, int lane) {
-  return lut[byte * kAttnLutCopies + (lane & 31)];
-}
-
 // NQ * 16 query rows of one wave: Q operand, running statistics, O^T.
 template <int FMT, int D, int NQ>
 struct AttnWave {
@@ -278,7 +271,15 @@ __device__ __forceinline__ void attn_tile(AttnWave<FMT, D, NQ> &w, AttnTile<FMT,
   constexpr bool MX = FMT == GNF4_MXFP4;
   constexpr int KS = D / 32, ND = D / 16;
   const int c = lane & 15, g = lane >> 4;
+  const uint32_t lane4 = (uint32_t)lane * 4;
   float s[NQ][8];
+  if constexpr (!MX) {                                       // absmax over the operand codebook's scale
+#pragma unroll
+    for (int i = 0; i < AttnTile<FMT, D>::SW; ++i) {
+      x.ks[i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, x.ks[i]) * kNF4InvScale);
+      x.vs[i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, x.vs[i]) * kNF4InvScale);
+    }
+  }
   // ---- scores of positions 8g..8g+7 for the lane's query row
   static_for<0, 2>([&](auto I) {
     constexpr int i = I;
@@ -293,8 +294,8 @@ __device__ __forceinline__ void attn_tile(AttnWave<FMT, D, NQ> &w, AttnTile<FMT,
         const float sc = e8m0_scale(D == 256 ? (k < KS / 2 ? x.ks[i] & 0xffu : x.ks[i] >> 8) : x.ks[i]);
         ka = op8(fp4_pair<0>(kw, sc), fp4_pair<1>(kw, sc), fp4_pair<2>(kw, sc), fp4_pair<3>(kw, sc));
       } else {
-        ka = op8(nf4_lut32(lut, kw & 0xffu, lane), nf4_lut32(lut, (kw >> 8) & 0xffu, lane),
-                 nf4_lut32(lut, (kw >> 16) & 0xffu, lane), nf4_lut32(lut, kw >> 24, lane));
+        ka = op8(lut_read(lut, lut_addr(kw, lane4, 0)), lut_read(lut, lut_addr(kw, lane4, 1)),
+                 lut_read(lut, lut_addr(kw, lane4, 2)), lut_read(lut, lut_addr(kw, lane4, 3)));
       }
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
@@ -315,7 +316,7 @@ __device__ __forceinline__ void attn_tile(AttnWave<FMT, D, NQ> &w, AttnTile<FMT,
 #pragma unroll
     for (int n = 0; n < NQ; ++n)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) s[n][4 * i + j] = acc[n][j] * a.scale_log2;
+      for (int j = 0; j < 4; ++j) s[n][4 * i + j] = acc[n][j];
   });
   // ---- mask, running maximum, probabilities
   uint32_t see[NQ];
@@ -336,7 +337,7 @@ __device__ __forceinline__ void attn_tile(AttnWave<FMT, D, NQ> &w, AttnTile<FMT,
     float mx = s[n][0];
 #pragma unroll
     for (int j = 1; j < 8; ++j) mx = fmaxf(mx, s[n][j]);
-    mx = max_xor16_32(mx);
+    mx = max_xor16_32(mx) * a.scale_log2;
     // m is raised only when it has fallen 2^8 behind: until then the
     // probabilities are up to 256 instead of 1, which costs no accuracy in
     // float32 or bf16, and the sums need not be rescaled.
@@ -352,7 +353,7 @@ __device__ __forceinline__ void attn_tile(AttnWave<FMT, D, NQ> &w, AttnTile<FMT,
     float sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      s[n][j] = __builtin_amdgcn_exp2f(s[n][j] - ms);
+      s[n][j] = __builtin_amdgcn_exp2f(fmaf(s[n][j], a.scale_log2, -ms));
       sum += s[n][j];
     }
     w.l[n] += sum;
@@ -439,7 +440,7 @@ __device__ __forceinline__ void attn_tile(AttnWave<FMT, D, NQ> &w, AttnTile<FMT,
       for (int y = 0; y < 2; ++y) {
         uint32_t pr[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) pr[j] = nf4_lut32(lut, y ? x.vc[j][b] >> 8 : x.vc[j][b] & 0xffu, lane);
+        for (int j = 0; j < 8; ++j) pr[j] = lut_read(lut, lut_addr(x.vc[j][b], lane4, y));
         uint32_t e[4], f[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -502,7 +503,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void kv_attn_kernel(KvAttnArgs a) 
   constexpr int NT = 64 * NW, ROUND = 32 * NW;
   constexpr int KS = D / 32, ND = D / 16, M = 16 * NQ;
   constexpr int DC = D < 128 ? D : 128;                      // values of a row joined at a time
-  constexpr int LUT = MX ? 0 : 256 * kAttnLutCopies;
+  constexpr int LUT = MX ? 0 : kLutWords;
   constexpr int DEPTH = D == 256 || NQ > 1 ? 2 : 3;          // tiles in registers: one computed, the others in flight
   __shared__ __attribute__((aligned(16))) uint32_t lut[LUT ? LUT : 4];
   __shared__ __attribute__((aligned(16))) float red[NW * 16 * (DC + 4)];
@@ -513,13 +514,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void kv_attn_kernel(KvAttnArgs a) 
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = lane & 15, g = lane >> 4;
   const int Hq = kv.H * a.G;
   if constexpr (!MX) {
-    // entry b, copies 4j..4j+3 as one 16-byte store
-#pragma unroll 4
-    for (int i = tid; i < 256 * kAttnLutCopies / 4; i += NT) {
-      const uint32_t e = (uint32_t)i / (kAttnLutCopies / 4);
-      const uint32_t v = nf4_bf16(e >> 4) | (nf4_bf16(e & 15u) << 16);
-      *reinterpret_cast<uint4 *>(lut + 4 * i) = make_uint4(v, v, v, v);
-    }
+    fill_nf4_lut<NT>(lut, tid);
     __syncthreads();
   }
 
@@ -625,6 +620,10 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void kv_attn_kernel(KvAttnArgs a) 
         const int d = MX ? g * (D / 4) + k * 8 : (k >> 1) * 64 + g * 16 + (k & 1) * 8;
         uint4 v = make_uint4(0, 0, 0, 0);
         if (ok) v = *reinterpret_cast<const uint4 *>(qp + d);
+        v.x ^= a.q_sign;
+        v.y ^= a.q_sign;
+        v.z ^= a.q_sign;
+        v.w ^= a.q_sign;
         w.q[n][k] = __builtin_bit_cast(bf16x8_t, v);
       }
 #pragma unroll
@@ -792,28 +791,29 @@ __global__ __launch_bounds__(kJoinThreads) void kv_attn_join_kernel(KvAttnArgs a
 }
 
 // Rows per tile from the most new tokens of a sequence. Short contexts, of up
-// to four rounds, take a workgroup per problem and one launch.
+// to four rounds, take a workgroup per problem and one launch; where these are
+// at least as many as compute units, of four waves, so that two fit on one.
 bool kv_attention_plan(int32_t D, int32_t H, int32_t G, int32_t B, int64_t n_tokens, int32_t max_new,
                        int64_t max_len, int32_t window, KvAttnPlan *p) {
   const int64_t rows = (int64_t)max_new * G;
   p->nq = rows <= 16 || D == 256 ? 1 : 2;                     // D = 256: the registers hold no second tile
   p->waves = p->nq == 1 && D <= 128 ? 8 : 4;
-  const int round = 32 * p->waves;
+  int round = 32 * p->waves;
   const int M = 16 * p->nq;
   const int64_t n_mt = (rows + M - 1) / M;
   p->items = (int64_t)B * n_mt * H;
   int64_t len = std::max<int64_t>(max_len, 1);
-  if (window > 0) len = std::min<int64_t>(len, (int64_t)window + max_new - 1 + round - 1);
+  if (window > 0) len = std::min<int64_t>(len, (int64_t)window + max_new - 1 + 31);
   if (p->items > 0x7fffffffLL) return false;
   p->n_mt = (int32_t)n_mt;
   p->shared = len > 4 * round;
+  if (!p->shared && p->items >= kAttnGroups) p->waves = 4;
   p->bytes = p->shared ? (size_t)(2 * kAttnGroups * M) * (D + 2) * 4 : 0;
   return true;
 }
 
-template <int FMT, int D, int NQ>
+template <int FMT, int D, int NQ, int NW>
 static hipError_t attn_go(const KvAttnArgs &a, const KvAttnPlan &p, hipStream_t s) {
-  constexpr int NW = NQ == 1 && D <= 128 ? 8 : 4;
   hipLaunchKernelGGL((kv_attn_kernel<FMT, D, NQ, NW>), dim3(p.shared ? kAttnGroups : (unsigned)p.items), dim3(64 * NW),
                      0, s, a);
   hipError_t e = hipGetLastError();
@@ -825,15 +825,21 @@ static hipError_t attn_go(const KvAttnArgs &a, const KvAttnPlan &p, hipStream_t 
 template <int FMT, int D>
 static hipError_t attn_nq(const KvAttnArgs &a, const KvAttnPlan &p, hipStream_t s) {
   if constexpr (D <= 128) {
-    if (p.nq == 2) return attn_go<FMT, D, 2>(a, p, s);
+    if (p.nq == 2) return attn_go<FMT, D, 2, 4>(a, p, s);
+    if (p.waves == 8) return attn_go<FMT, D, 1, 8>(a, p, s);
   }
-  return attn_go<FMT, D, 1>(a, p, s);
+  return attn_go<FMT, D, 1, 4>(a, p, s);
 }
 
 hipError_t launch_kv_attention(const KvAttnArgs &args, const KvAttnPlan &p, int32_t format, hipStream_t s) {
   KvAttnArgs a = args;
   a.n_mt = p.n_mt;
   a.shared = p.shared;
+  // The running maximum is taken before the scale, which therefore must not be
+  // negative (the queries change sign instead) nor 0 (0 times the -inf of a
+  // masked place; 2^-100 leaves the weights equal).
+  a.q_sign = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
+  a.scale_log2 = std::max(std::fabs(a.scale_log2), 0x1p-100f);
   if (format == GNF4_MXFP4) {
     if (a.kv.D == 64) return attn_nq<GNF4_MXFP4, 64>(a, p, s);
     if (a.kv.D == 128) return attn_nq<GNF4_MXFP4, 128>(a, p, s);

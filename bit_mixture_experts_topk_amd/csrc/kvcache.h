@@ -34,6 +34,7 @@ struct KvAttnArgs {
   int32_t G;                      // query heads per cache head
   int32_t window;                 // 0: none
   float scale_log2;               // scale * log2(e): the softmax runs in base 2
+  uint32_t q_sign;                // flips the queries' signs (a negative scale)
   int32_t n_mt;                   // most row tiles of one sequence
   int32_t shared;                 // 1: equal shares of all work per workgroup; 0: a workgroup per tile
   float *part;                    // [slots][M][D] then [slots][M][2], two slots per workgroup
