@@ -123,38 +123,31 @@ __device__ __forceinline__ uint32_t row_bcast(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x150 + N, 0xf, 0xf, false);
 }
 
-__device__ __forceinline__ int attn_page(const KvView &kv, int b, int pos) {
-  return kv.pages[(int64_t)b * kv.max_pages + min(pos >> kv.page_shift, kv.max_pages - 1)];
-}
-
-// Page ids of the wave's tile at position t: the lane's K rows and V rows.
+// Pages of the wave's tile at position t: of its first and of its last 16
+// positions (pages hold 16 at least).
 struct AttnPages {
-  int k, v;
+  int a, b;
 };
 
-__device__ __forceinline__ AttnPages attn_pages(const KvView &kv, int b, int t, int lane) {
+__device__ __forceinline__ AttnPages attn_pages(const KvView &kv, int b, int t) {
+  const int32_t *row = kv.pages + (int64_t)b * kv.max_pages;
   AttnPages p;
-  p.k = attn_page(kv, b, t + ((lane & 15) >> 2) * 8);
-  p.v = attn_page(kv, b, t + (lane >> 4) * 8);
+  p.a = row[min(t >> kv.page_shift, kv.max_pages - 1)];
+  p.b = row[min((t + 16) >> kv.page_shift, kv.max_pages - 1)];
   return p;
 }
 
-template <int FMT, int D>
-__device__ __forceinline__ void attn_load(AttnTile<FMT, D> &x, const KvView &kv, int h, int t, AttnPages p,
-                                          int lane) {
+// The loads of a tile from the addresses of its lanes: krow / vrow are the K
+// and V rows of the lane's group (a position 8 (r / 4) and 8 g of the tile).
+template <int FMT, int D, class Row>
+__device__ __forceinline__ void attn_load_at(AttnTile<FMT, D> &x, const KvView &kv, Row at, int lane) {
   typedef AttnTile<FMT, D> T;
-  const int r = lane & 15, g = lane >> 4, mask = (1 << kv.page_shift) - 1;
-  x.bad = (uint32_t)p.v >= (uint32_t)kv.n_pages;
-  // an id outside the cache reads page 0 and is masked
-  const int pk = (uint32_t)p.k >= (uint32_t)kv.n_pages ? 0 : p.k, pv = x.bad ? 0 : p.v;
-  const int kt = t + (r >> 2) * 8 + (r & 3), vt = t + g * 8;
-  const int64_t krow = (((int64_t)pk * kv.H + h) << kv.page_shift) + (kt & mask);
-  const int64_t vrow = (((int64_t)pv * kv.H + h) << kv.page_shift) + (vt & mask);
-  const uint8_t *kp = kv.k_codes + krow * (D / 2), *vp = kv.v_codes + vrow * (D / 2);
+  const int r = lane & 15, g = lane >> 4;
+  const uint32_t kt = (uint32_t)((r >> 2) * 8 + (r & 3)), vt = (uint32_t)(g * 8);
   if constexpr (T::MX) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const uint8_t *s = kp + i * 4 * (D / 2) + g * (D / 8);
+      const uint8_t *s = at(kv.k_codes, D / 2, r >> 2, (kt + i * 4) * (D / 2) + g * (D / 8));
       if constexpr (D == 64) {
         const uint2 v = *reinterpret_cast<const uint2 *>(s);
         x.kc[i][0] = v.x;
@@ -169,12 +162,12 @@ __device__ __forceinline__ void attn_load(AttnTile<FMT, D> &x, const KvView &kv,
           x.kc[i][w + 3] = v.w;
         }
       }
-      const uint8_t *sc = static_cast<const uint8_t *>(kv.k_scales) + (krow + i * 4) * (D / 32);
-      if constexpr (D == 64) x.ks[i] = sc[g >> 1];
-      else if constexpr (D == 128) x.ks[i] = sc[g];
-      else x.ks[i] = *reinterpret_cast<const uint16_t *>(sc + 2 * g);
+      const uint8_t *sc = at(static_cast<const uint8_t *>(kv.k_scales), D / 32, r >> 2,
+                             (kt + i * 4) * (D / 32) + (D == 64 ? g >> 1 : D == 128 ? g : 2 * g));
+      if constexpr (D == 256) x.ks[i] = *reinterpret_cast<const uint16_t *>(sc);
+      else x.ks[i] = *sc;
     }
-    const uint8_t *sv = static_cast<const uint8_t *>(kv.v_scales) + (vrow + (r & 7)) * (D / 32);
+    const uint8_t *sv = at(static_cast<const uint8_t *>(kv.v_scales), D / 32, g, (vt + (r & 7)) * (D / 32));
     if constexpr (D == 64) x.vs[0] = *reinterpret_cast<const uint16_t *>(sv);
     else if constexpr (D == 128) x.vs[0] = *reinterpret_cast<const uint32_t *>(sv);
     else {
@@ -182,9 +175,10 @@ __device__ __forceinline__ void attn_load(AttnTile<FMT, D> &x, const KvView &kv,
       x.vs[0] = v.x;
       x.vs[1] = v.y;
     }
+    const uint8_t *vp = at(kv.v_codes, D / 2, g, vt * (D / 2) + r * (D / 32));
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const uint8_t *s = vp + j * (D / 2) + r * (D / 32);
+      const uint8_t *s = vp + j * (D / 2);
       if constexpr (D == 64) x.vc[j][0] = *reinterpret_cast<const uint16_t *>(s);
       else if constexpr (D == 128) x.vc[j][0] = *reinterpret_cast<const uint32_t *>(s);
       else {
@@ -196,31 +190,57 @@ __device__ __forceinline__ void attn_load(AttnTile<FMT, D> &x, const KvView &kv,
   } else {
     // block b of 64: lane group g takes values 16 g .. 16 g + 15 of it (K),
     // lane c values 4 c .. 4 c + 3 (V)
+    const uint8_t *kp = at(kv.k_codes, D / 2, r >> 2, kt * (D / 2) + g * 8);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int b = 0; b < D / 64; ++b) {
-        const uint2 v = *reinterpret_cast<const uint2 *>(kp + i * 4 * (D / 2) + b * 32 + g * 8);
+        const uint2 v = *reinterpret_cast<const uint2 *>(kp + i * 4 * (D / 2) + b * 32);
         x.kc[i][2 * b] = v.x;
         x.kc[i][2 * b + 1] = v.y;
       }
     // absmax of positions 8g..8g+7: D/8 words, word w in lane w % 16 of the row
     // (D = 64: lanes 8..15 repeat lanes 0..7)
-    const int w = D == 64 ? r & 7 : r;
-    const int64_t krow8 = (((int64_t)pv * kv.H + h) << kv.page_shift) + (vt & mask);
-    const uint32_t *ks = static_cast<const uint32_t *>(kv.k_scales) + krow8 * (D / 64) + w;
-    const uint32_t *vs = static_cast<const uint32_t *>(kv.v_scales) + vrow * (D / 64) + w;
-    x.ks[0] = ks[0];
-    x.vs[0] = vs[0];
+    const uint32_t w = vt * (D / 16) + 4 * (D == 64 ? r & 7 : r);
+    const uint8_t *ks = at(static_cast<const uint8_t *>(kv.k_scales), D / 16, g, w);
+    const uint8_t *vs = at(static_cast<const uint8_t *>(kv.v_scales), D / 16, g, w);
+    x.ks[0] = *reinterpret_cast<const uint32_t *>(ks);
+    x.vs[0] = *reinterpret_cast<const uint32_t *>(vs);
     if constexpr (D == 256) {
-      x.ks[1] = ks[16];
-      x.vs[1] = vs[16];
+      x.ks[1] = *reinterpret_cast<const uint32_t *>(ks + 64);
+      x.vs[1] = *reinterpret_cast<const uint32_t *>(vs + 64);
     }
+    const uint8_t *vp = at(kv.v_codes, D / 2, g, vt * (D / 2) + r * 2);
 #pragma unroll
     for (int j = 0; j < 8; ++j)
 #pragma unroll
       for (int b = 0; b < D / 64; ++b)
-        x.vc[j][b] = *reinterpret_cast<const uint16_t *>(vp + j * (D / 2) + b * 32 + r * 2);
+        x.vc[j][b] = *reinterpret_cast<const uint16_t *>(vp + j * (D / 2) + b * 32);
+  }
+}
+
+// Page ids are the same for the whole wave, so rows are found with scalar
+// arithmetic: of both halves of the tile, equal where a page covers it all.
+template <int FMT, int D>
+__device__ __forceinline__ void attn_load(AttnTile<FMT, D> &x, const KvView &kv, int h, int t, AttnPages p,
+                                          int lane) {
+  const int mask = (1 << kv.page_shift) - 1;
+  int pa = __builtin_amdgcn_readfirstlane(p.a), pb = __builtin_amdgcn_readfirstlane(p.b);
+  const bool bada = (uint32_t)pa >= (uint32_t)kv.n_pages, badb = (uint32_t)pb >= (uint32_t)kv.n_pages;
+  x.bad = (lane >> 5) ? badb : bada;
+  // an id outside the cache reads page 0 and is masked
+  pa = bada ? 0 : pa;
+  pb = badb ? 0 : pb;
+  const int64_t ra = (((int64_t)pa * kv.H + h) << kv.page_shift) + (t & mask);
+  if (kv.page_shift > 4) {
+    attn_load_at<FMT, D>(x, kv, [&](const uint8_t *base, int size, int, uint32_t off) {
+      return base + ra * size + off;
+    }, lane);
+  } else {
+    const int64_t rb = (((int64_t)pb * kv.H + h) << kv.page_shift) + ((t + 16) & mask) - 16;
+    attn_load_at<FMT, D>(x, kv, [&](const uint8_t *base, int size, int group, uint32_t off) {
+      return base + (group < 2 ? ra : rb) * size + off;
+    }, lane);
   }
 }
 
@@ -284,8 +304,6 @@ __device__ __forceinline__ void attn_tile(AttnWave<FMT, D, NQ> &w, AttnTile<FMT,
   static_for<0, 2>([&](auto I) {
     constexpr int i = I;
     f32x4_t acc[NQ], blk[NQ];
-#pragma unroll
-    for (int n = 0; n < NQ; ++n) acc[n] = blk[n] = f32x4_t{0, 0, 0, 0};
     static_for<0, KS>([&](auto K) {
       constexpr int k = K;
       bf16x8_t ka;
@@ -299,18 +317,19 @@ __device__ __forceinline__ void attn_tile(AttnWave<FMT, D, NQ> &w, AttnTile<FMT,
       }
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
-        if constexpr (MX) acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ka, w.q[n][k], acc[n], 0, 0, 0);
-        else blk[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ka, w.q[n][k], blk[n], 0, 0, 0);
+        constexpr f32x4_t zero = {0, 0, 0, 0};
+        if constexpr (MX)
+          acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ka, w.q[n][k], k == 0 ? zero : acc[n], 0, 0, 0);
+        else
+          blk[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ka, w.q[n][k], (k & 1) == 0 ? zero : blk[n], 0, 0, 0);
       }
       if constexpr (!MX && (k & 1)) {                        // a block of 64 is complete
         static_for<0, 4>([&](auto J) {
           constexpr int j = J;
           const float ab = nf4_absmax<D, 4 * i + j, k / 2>(x.ks);
 #pragma unroll
-          for (int n = 0; n < NQ; ++n) acc[n][j] = fmaf(blk[n][j], ab, acc[n][j]);
+          for (int n = 0; n < NQ; ++n) acc[n][j] = k == 1 ? blk[n][j] * ab : fmaf(blk[n][j], ab, acc[n][j]);
         });
-#pragma unroll
-        for (int n = 0; n < NQ; ++n) blk[n] = f32x4_t{0, 0, 0, 0};
       }
     });
 #pragma unroll
@@ -341,7 +360,7 @@ __device__ __forceinline__ void attn_tile(AttnWave<FMT, D, NQ> &w, AttnTile<FMT,
     // m is raised only when it has fallen 2^8 behind: until then the
     // probabilities are up to 256 instead of 1, which costs no accuracy in
     // float32 or bf16, and the sums need not be rescaled.
-    if (__any(mx > w.m[n] + 8.0f)) {
+    if (__builtin_expect(__any(mx > w.m[n] + 8.0f), 0)) {
       mx = fmaxf(mx, w.m[n]);
       const float alpha = __builtin_amdgcn_exp2f(w.m[n] - (mx == kNegInf ? 0.0f : mx));
       w.m[n] = mx;
@@ -504,12 +523,20 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void kv_attn_kernel(KvAttnArgs a) 
   constexpr int KS = D / 32, ND = D / 16, M = 16 * NQ;
   constexpr int DC = D < 128 ? D : 128;                      // values of a row joined at a time
   constexpr int LUT = MX ? 0 : kLutWords;
-  constexpr int DEPTH = D == 256 || NQ > 1 ? 2 : 3;          // tiles in registers: one computed, the others in flight
-  __shared__ __attribute__((aligned(16))) uint32_t lut[LUT ? LUT : 4];
-  __shared__ __attribute__((aligned(16))) float red[NW * 16 * (DC + 4)];
-  __shared__ float sm[NW][M], sl[NW][M];
-  __shared__ int64_t pre[NT + 1];
-  __shared__ int64_t wsum[NW];
+  constexpr int DEPTH = D == 256 || NQ > 1 || (!MX && D == 128) ? 2 : 3;          // tiles in registers: one computed, the others in flight
+  // one block, so that the table starts at LDS address 0 and a byte's address
+  // is what lut_addr forms
+  struct Lds {
+    uint32_t lut[LUT ? LUT : 4];
+    float red[NW * 16 * (DC + 4)];
+    float sm[NW][M], sl[NW][M];
+    int64_t pre[NT + 1], wsum[NW];
+  };
+  __shared__ __attribute__((aligned(16))) Lds lds;
+  uint32_t *lut = lds.lut;
+  float *red = lds.red;
+  auto &sm = lds.sm, &sl = lds.sl;
+  int64_t *pre = lds.pre, *wsum = lds.wsum;
   const KvView &kv = a.kv;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = lane & 15, g = lane >> 4;
   const int Hq = kv.H * a.G;
@@ -638,7 +665,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void kv_attn_kernel(KvAttnArgs a) 
     if (t < t1) {
       // DEPTH - 1 rounds ahead the codes are in flight, one more the page ids
 #pragma unroll
-      for (int i = 0; i < DEPTH; ++i) pg[i] = attn_pages(kv, bb, t + i * ROUND, lane);
+      for (int i = 0; i < DEPTH; ++i) pg[i] = attn_pages(kv, bb, t + i * ROUND);
 #pragma unroll
       for (int i = 0; i < DEPTH - 1; ++i)
         if (t + i * ROUND < t1) attn_load<FMT, D>(tl[i], kv, h, t + i * ROUND, pg[i], lane);
@@ -646,7 +673,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void kv_attn_kernel(KvAttnArgs a) 
 #pragma unroll
         for (int i = 0; i < DEPTH; ++i) {
           constexpr int A = DEPTH - 1;
-          pg[i] = attn_pages(kv, bb, t + DEPTH * ROUND, lane);
+          pg[i] = attn_pages(kv, bb, t + DEPTH * ROUND);
           if (t + A * ROUND < t1)
             attn_load<FMT, D>(tl[(i + A) % DEPTH], kv, h, t + A * ROUND, pg[(i + A) % DEPTH], lane);
           const bool all = t >= full_lo && t + 31 <= full_hi && __ballot(tl[i].bad) == 0;
