@@ -12,27 +12,33 @@
 //
 // Tiling. The query heads that share a cache head, for all new tokens of a
 // sequence, are the rows of one problem (row = token * G + g), cut into tiles
-// of 16 * NQ rows. A workgroup's NW waves take 32 positions each, 32 * NW a
-// round, and join at the end of a tile through LDS. NW is 8 where a wave's
-// registers allow two waves per SIMD, else 4.
-// Sequences differ in length, so the rounds of all (sequence, tile, head)
-// problems are numbered through and every workgroup, one per compute unit,
-// takes an equal run of them, over the end of one problem into the next. A
-// problem that lies in several runs is put together by a second kernel.
-// Registers only, no transposes. v_mfma_f32_16x16x32_bf16 takes A rows from
-// lanes 0..15 with 8 consecutive k per lane group g = lane / 16, and leaves C
-// with its column in the lane and rows 4g..4g+3 in the registers. Computed are
-// S^T = K Q^T (rows = positions, columns = query rows) and O^T = V^T P^T. Row r
-// of K tile i (of two) is position 8 (r / 4) + 4 i + r % 4 of the 32, so the
-// scores that a lane holds after both tiles are those of positions 8g..8g+7,
-// which are just the k indices that it has to supply of P^T: the
-// probabilities go from one product to the next without leaving their lane,
-// and so does the softmax, whose row is the lane's column.
+// of 16 * NQ rows. A workgroup's NW waves take 32 positions each in turn and
+// join at the end of a problem through LDS.
+// Sequences differ in length, so the runs of 128 positions of all (sequence,
+// tile, head) problems are numbered through and every workgroup, one per
+// compute unit, takes an equal share of them, over the end of one problem into
+// the next. A problem that lies in several shares is put together by a second
+// kernel.
+//
+// Bound by the cache's bytes: a wave keeps its next tiles in flight straight
+// into LDS (global_load_lds, no registers), S slots of its own, so that a
+// compute unit has about 70 KB under way and its registers hold four waves per
+// SIMD, which cover each other's latencies.
+//
+// No transposes. v_mfma_f32_16x16x32_bf16 takes A rows from lanes 0..15 with 8
+// consecutive k per lane group g = lane / 16, and leaves C with its column in
+// the lane and rows 4g..4g+3 in the registers. Computed are S^T = K Q^T (rows =
+// positions, columns = query rows) and O^T = V^T P^T. Row r of K tile i (of
+// two) is position 8 (r / 4) + 4 i + r % 4 of the 32, so the scores that a lane
+// holds after both tiles are those of positions 8g..8g+7, which are just the k
+// indices that it has to supply of P^T: the probabilities go from one product
+// to the next without leaving their lane, and so does the softmax, whose row is
+// the lane's column.
 // The k order of S is free as well: MXFP4 lane group g takes values g D/4 ..
-// (g+1) D/4 of the head, so that one load brings its codes and (D = 128) they
-// share one scale. V^T rows are columns of the cache, so lane c reads its
-// D/16 values of every one of 8 positions and pairs of positions are put
-// together after decoding.
+// (g+1) D/4 of the head (D = 128: one 16-byte piece and one scale), NF4 16 of
+// every block of 64. V^T rows are columns of the cache: lane c reads its values
+// of each of 8 positions, and pairs of positions are put together after
+// decoding.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -77,13 +83,20 @@ struct AttnSeq {
   int r0, rows;                   // first token row, query rows (tokens * G)
   int start;                      // position of its first new token
   int lo, hi;                     // positions that any row may see, lo a multiple of 32
-  int mts, units;                 // row tiles; rounds per tile and head (at least one: it writes the result)
+  int mts, units;                 // row tiles; runs of 128 positions per tile and head (at least one: it
+                                  // writes the result)
 };
 
-__device__ __forceinline__ AttnSeq attn_seq(const KvAttnArgs &a, int b, int M, int round) {
+constexpr int kAttnUnit = 128;
+
+// Arrays that no kernel writes meanwhile: scalar loads where the index is uniform.
+typedef const __attribute__((address_space(4))) int32_t *const_ints;
+
+__device__ __forceinline__ AttnSeq attn_seq(const KvAttnArgs &a, int b, int M) {
   const KvView &kv = a.kv;
   AttnSeq x;
-  const int o0 = kv.offsets[b], o1 = kv.offsets[b + 1], len = kv.lens[b];
+  const const_ints off = (const_ints)(uintptr_t)kv.offsets, lens = (const_ints)(uintptr_t)kv.lens;
+  const int o0 = off[b], o1 = off[b + 1], len = lens[b];
   const int e = min(max(o1, 0), kv.n_tokens);
   x.r0 = min(max(o0, 0), e);
   const int n = e - x.r0;
@@ -92,30 +105,30 @@ __device__ __forceinline__ AttnSeq attn_seq(const KvAttnArgs &a, int b, int M, i
   x.hi = (int)min((int64_t)len, (int64_t)kv.max_pages << kv.page_shift);
   x.lo = a.window > 0 ? max(0, x.start - a.window + 1) & ~31 : 0;
   x.mts = min((x.rows + M - 1) / M, a.n_mt);
-  x.units = x.hi > x.lo ? (x.hi - x.lo + round - 1) / round : 1;
+  x.units = x.hi > x.lo ? (x.hi - x.lo + kAttnUnit - 1) / kAttnUnit : 1;
   return x;
 }
 
-__device__ __forceinline__ int64_t attn_units(const KvAttnArgs &a, int b, int M, int round) {
-  const AttnSeq x = attn_seq(a, b, M, round);
-  return (int64_t)x.mts * a.kv.H * x.units;
+// Sum over the wave's lanes up to and with this one (DPP shifts within rows of
+// 16, then the last lanes of the rows before).
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);
+  return v;
 }
 
-// One wave's 32 positions: raw codes and scales in registers. The scales of
-// positions 8g..8g+7 lie in lane group g's own row of 16 lanes, read there
-// with a row broadcast where they are used.
-template <int FMT, int D>
-struct AttnTile {
-  static constexpr bool MX = FMT == GNF4_MXFP4;
-  static constexpr int KW = D / 32;                          // code dwords per lane and K tile
-  static constexpr int VW = MX ? (D == 256 ? 2 : 1) : D / 64;  // code pieces per lane and position
-  static constexpr int SW = MX ? (D == 256 ? 2 : 1) : (D == 256 ? 2 : 1);
-  uint32_t kc[2][KW];
-  uint32_t ks[2];                 // MXFP4: scale byte(s) of the lane's K rows; NF4: words of absmax
-  uint32_t vc[8][VW];
-  uint32_t vs[SW];                // MXFP4: scale bytes of position 8g + c % 8; NF4: words of absmax
-  bool bad;                       // positions 8g..8g+7 lie on no page
-};
+__device__ __forceinline__ int attn_units(const KvAttnArgs &a, const AttnSeq &x) { return x.mts * a.kv.H * x.units; }
+
+// Running sum of the units of the 64 sequences from b0 on, one per lane.
+__device__ __forceinline__ int attn_sums(const KvAttnArgs &a, int b0, int M, int lane) {
+  const int b = b0 + lane;
+  const AttnSeq x = attn_seq(a, min(b, a.kv.B - 1), M);
+  return wave_scan(b < a.kv.B ? attn_units(a, x) : 0);
+}
 
 // Lane N of the lane's row of 16.
 template <int N>
@@ -123,137 +136,133 @@ __device__ __forceinline__ uint32_t row_bcast(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x150 + N, 0xf, 0xf, false);
 }
 
-// Pages of the wave's tile at position t: of its first and of its last 16
-// positions (pages hold 16 at least).
+// ------------------------------------------------------- a tile's way into LDS
+
+// 16 or 4 bytes per lane from base + off (or p) to LDS address lds + lane * 16
+// (4). Counted by vmcnt; nothing is returned to registers.
+__device__ __forceinline__ void dma16(const uint8_t *base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
+               : "memory", "m0");
+}
+__device__ __forceinline__ void dma16(const uint8_t *p, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(p) : "memory", "m0");
+}
+__device__ __forceinline__ void dma4(const uint8_t *base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(off), "s"(base)
+               : "memory", "m0");
+}
+__device__ __forceinline__ void dma4(const uint8_t *p, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(p) : "memory", "m0");
+}
+
+// Waits until at most N of the wave's loads are under way.
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// A slot: 32 positions' codes of K (in the order the lanes read them), of V
+// (row 4j + g holds position 8g + j, so that lane (c, g) reads along a line),
+// and the scales of both.
+template <int FMT, int D>
+struct AttnSlot {
+  static constexpr bool MX = FMT == GNF4_MXFP4;
+  static constexpr int CH = D / 32;                          // 16-byte pieces per row
+  static constexpr int N16 = CH / 2;                         // loads of 1 KB per side
+  static constexpr int SC = MX ? D : 2 * D;                  // scale bytes per side
+  static constexpr int VOFF = 16 * D, SOFF = 32 * D;
+  static constexpr int BYTES = 32 * D + (2 * SC < 256 ? 256 : 2 * SC);
+  static constexpr int LOADS = 2 * N16 + (SC == 256 ? 2 : 1);
+};
+
+// Page ids of a tile: of its first and last 16 positions (pages hold 16 at least).
 struct AttnPages {
   int a, b;
 };
 
 __device__ __forceinline__ AttnPages attn_pages(const KvView &kv, int b, int t) {
-  const int32_t *row = kv.pages + (int64_t)b * kv.max_pages;
+  const_ints row = (const_ints)(uintptr_t)(kv.pages + (int64_t)b * kv.max_pages);
   AttnPages p;
   p.a = row[min(t >> kv.page_shift, kv.max_pages - 1)];
   p.b = row[min((t + 16) >> kv.page_shift, kv.max_pages - 1)];
   return p;
 }
 
-// The loads of a tile from the addresses of its lanes: krow / vrow are the K
-// and V rows of the lane's group (a position 8 (r / 4) and 8 g of the tile).
-template <int FMT, int D, class Row>
-__device__ __forceinline__ void attn_load_at(AttnTile<FMT, D> &x, const KvView &kv, Row at, int lane) {
-  typedef AttnTile<FMT, D> T;
-  const int r = lane & 15, g = lane >> 4;
-  const uint32_t kt = (uint32_t)((r >> 2) * 8 + (r & 3)), vt = (uint32_t)(g * 8);
-  if constexpr (T::MX) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint8_t *s = at(kv.k_codes, D / 2, r >> 2, (kt + i * 4) * (D / 2) + g * (D / 8));
-      if constexpr (D == 64) {
-        const uint2 v = *reinterpret_cast<const uint2 *>(s);
-        x.kc[i][0] = v.x;
-        x.kc[i][1] = v.y;
-      } else {
-#pragma unroll
-        for (int w = 0; w < T::KW; w += 4) {
-          const uint4 v = *reinterpret_cast<const uint4 *>(s + 4 * w);
-          x.kc[i][w] = v.x;
-          x.kc[i][w + 1] = v.y;
-          x.kc[i][w + 2] = v.z;
-          x.kc[i][w + 3] = v.w;
-        }
-      }
-      const uint8_t *sc = at(static_cast<const uint8_t *>(kv.k_scales), D / 32, r >> 2,
-                             (kt + i * 4) * (D / 32) + (D == 64 ? g >> 1 : D == 128 ? g : 2 * g));
-      if constexpr (D == 256) x.ks[i] = *reinterpret_cast<const uint16_t *>(sc);
-      else x.ks[i] = *sc;
-    }
-    const uint8_t *sv = at(static_cast<const uint8_t *>(kv.v_scales), D / 32, g, (vt + (r & 7)) * (D / 32));
-    if constexpr (D == 64) x.vs[0] = *reinterpret_cast<const uint16_t *>(sv);
-    else if constexpr (D == 128) x.vs[0] = *reinterpret_cast<const uint32_t *>(sv);
-    else {
-      const uint2 v = *reinterpret_cast<const uint2 *>(sv);
-      x.vs[0] = v.x;
-      x.vs[1] = v.y;
-    }
-    const uint8_t *vp = at(kv.v_codes, D / 2, g, vt * (D / 2) + r * (D / 32));
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint8_t *s = vp + j * (D / 2);
-      if constexpr (D == 64) x.vc[j][0] = *reinterpret_cast<const uint16_t *>(s);
-      else if constexpr (D == 128) x.vc[j][0] = *reinterpret_cast<const uint32_t *>(s);
-      else {
-        const uint2 v = *reinterpret_cast<const uint2 *>(s);
-        x.vc[j][0] = v.x;
-        x.vc[j][1] = v.y;
-      }
-    }
-  } else {
-    // block b of 64: lane group g takes values 16 g .. 16 g + 15 of it (K),
-    // lane c values 4 c .. 4 c + 3 (V)
-    const uint8_t *kp = at(kv.k_codes, D / 2, r >> 2, kt * (D / 2) + g * 8);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int b = 0; b < D / 64; ++b) {
-        const uint2 v = *reinterpret_cast<const uint2 *>(kp + i * 4 * (D / 2) + b * 32);
-        x.kc[i][2 * b] = v.x;
-        x.kc[i][2 * b + 1] = v.y;
-      }
-    // absmax of positions 8g..8g+7: D/8 words, word w in lane w % 16 of the row
-    // (D = 64: lanes 8..15 repeat lanes 0..7)
-    const uint32_t w = vt * (D / 16) + 4 * (D == 64 ? r & 7 : r);
-    const uint8_t *ks = at(static_cast<const uint8_t *>(kv.k_scales), D / 16, g, w);
-    const uint8_t *vs = at(static_cast<const uint8_t *>(kv.v_scales), D / 16, g, w);
-    x.ks[0] = *reinterpret_cast<const uint32_t *>(ks);
-    x.vs[0] = *reinterpret_cast<const uint32_t *>(vs);
-    if constexpr (D == 256) {
-      x.ks[1] = *reinterpret_cast<const uint32_t *>(ks + 64);
-      x.vs[1] = *reinterpret_cast<const uint32_t *>(vs + 64);
-    }
-    const uint8_t *vp = at(kv.v_codes, D / 2, g, vt * (D / 2) + r * 2);
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-#pragma unroll
-      for (int b = 0; b < D / 64; ++b)
-        x.vc[j][b] = *reinterpret_cast<const uint16_t *>(vp + j * (D / 2) + b * 32);
-  }
-}
-
-// Page ids are the same for the whole wave, so rows are found with scalar
-// arithmetic: of both halves of the tile, equal where a page covers it all.
+// Sends the tile at position t into the slot at LDS address lds. Returns which
+// halves of it lie on no page (bit 0, 1): these read page 0 and are masked.
 template <int FMT, int D>
-__device__ __forceinline__ void attn_load(AttnTile<FMT, D> &x, const KvView &kv, int h, int t, AttnPages p,
-                                          int lane) {
+__device__ __forceinline__ uint32_t attn_send(const KvView &kv, int h, int t, AttnPages p, uint32_t lds, int lane) {
+  typedef AttnSlot<FMT, D> T;
+  constexpr int RB = D / 2, SB = T::SC / 32;                 // bytes per row: codes, scales
   const int mask = (1 << kv.page_shift) - 1;
-  int pa = __builtin_amdgcn_readfirstlane(p.a), pb = __builtin_amdgcn_readfirstlane(p.b);
-  const bool bada = (uint32_t)pa >= (uint32_t)kv.n_pages, badb = (uint32_t)pb >= (uint32_t)kv.n_pages;
-  x.bad = (lane >> 5) ? badb : bada;
-  // an id outside the cache reads page 0 and is masked
-  pa = bada ? 0 : pa;
-  pb = badb ? 0 : pb;
+  const bool bada = (uint32_t)p.a >= (uint32_t)kv.n_pages, badb = (uint32_t)p.b >= (uint32_t)kv.n_pages;
+  const int pa = bada ? 0 : p.a, pb = badb ? 0 : p.b;
   const int64_t ra = (((int64_t)pa * kv.H + h) << kv.page_shift) + (t & mask);
+  const uint8_t *ks = static_cast<const uint8_t *>(kv.k_scales), *vs = static_cast<const uint8_t *>(kv.v_scales);
+  // K: LDS piece (i, q, r) = piece q of the row of tile i, lane r
+  constexpr int LCH = T::CH == 2 ? 1 : T::CH == 4 ? 2 : 3;
+  const int r = lane & 15;
+  const int ki = T::CH == 2 ? lane >> 5 : 0, kq = T::CH == 2 ? (lane >> 4) & 1 : lane >> 4;
+  const int ktok = (r >> 2) * 8 + ki * 4 + (r & 3);
+  // V: LDS row 4j + g; the first load's rows, CH pieces each
+  const int vrow = lane >> LCH, vq = lane & (T::CH - 1);
+  const int vtok = (vrow & 3) * 8 + (vrow >> 2);
+  constexpr int VSTEP = (64 / T::CH) / 4;                    // positions further per load
+  // scales: lanes of one load share both sides unless a side takes a load of its own
+  constexpr int SW = T::SC == 512 ? 16 : 4;                  // bytes per lane
+  constexpr int SL = T::SC / SW;                             // lanes per side
+  const int sside = T::SC == 256 ? 0 : (lane / SL) & 1, soff = (T::SC == 256 ? lane : lane % SL) * SW;
   if (kv.page_shift > 4) {
-    attn_load_at<FMT, D>(x, kv, [&](const uint8_t *base, int size, int, uint32_t off) {
-      return base + ra * size + off;
-    }, lane);
+    const uint8_t *kb = kv.k_codes + ra * RB, *vb = kv.v_codes + ra * RB;
+#pragma unroll
+    for (int n = 0; n < T::N16; ++n) {
+      const int step = T::CH == 8 ? (n >> 1) * 4 * RB + (n & 1) * 64 : n * 4 * RB;
+      dma16(kb + step, (uint32_t)(ktok * RB + kq * 16), lds + n * 1024);
+      dma16(vb + n * VSTEP * RB, (uint32_t)(vtok * RB + vq * 16), lds + T::VOFF + n * 1024);
+    }
+    if constexpr (T::SC == 256) {
+      dma4(ks + ra * SB, (uint32_t)soff, lds + T::SOFF);
+      dma4(vs + ra * SB, (uint32_t)soff, lds + T::SOFF + 256);
+    } else {
+      const uint8_t *q = (sside ? vs : ks) + ra * SB + soff;
+      if constexpr (SW == 16) dma16(q, lds + T::SOFF);
+      else dma4(q, lds + T::SOFF);
+    }
   } else {
-    const int64_t rb = (((int64_t)pb * kv.H + h) << kv.page_shift) + ((t + 16) & mask) - 16;
-    attn_load_at<FMT, D>(x, kv, [&](const uint8_t *base, int size, int group, uint32_t off) {
-      return base + (group < 2 ? ra : rb) * size + off;
-    }, lane);
+    // pages of 16: the second half of the tile lies on another one
+    const int64_t rb = ((int64_t)pb * kv.H + h) * 16 - 16;
+    const int64_t rk = (r >> 2) < 2 ? ra : rb, rv = (vrow & 3) < 2 ? ra : rb;
+    const int64_t rs = soff / SB < 16 ? ra : rb;
+    const uint8_t *kb = kv.k_codes + rk * RB + ktok * RB + kq * 16;
+    const uint8_t *vb = kv.v_codes + rv * RB + vtok * RB + vq * 16;
+#pragma unroll
+    for (int n = 0; n < T::N16; ++n) {
+      const int step = T::CH == 8 ? (n >> 1) * 4 * RB + (n & 1) * 64 : n * 4 * RB;
+      dma16(kb + step, lds + n * 1024);
+      dma16(vb + n * VSTEP * RB, lds + T::VOFF + n * 1024);
+    }
+    if constexpr (T::SC == 256) {
+      dma4(ks + rs * SB + soff, lds + T::SOFF);
+      dma4(vs + rs * SB + soff, lds + T::SOFF + 256);
+    } else {
+      const uint8_t *q = (sside ? vs : ks) + rs * SB + soff;
+      if constexpr (SW == 16) dma16(q, lds + T::SOFF);
+      else dma4(q, lds + T::SOFF);
+    }
   }
+  return (bada ? 1u : 0u) | (badb ? 2u : 0u);
 }
 
-// NF4: the absmax of position 8g + J, block B of the lane's group.
+// NF4: the absmax of position 8g + J, block B of the lane's group: word w of the
+// group's D/8 lies in lane w % 16 of its row of lanes.
 template <int D, int J, int B>
-__device__ __forceinline__ float nf4_absmax(const uint32_t *w) {
+__device__ __forceinline__ float nf4_absmax(const float *w) {
   constexpr int at = J * (D / 64) + B;
-  return __builtin_bit_cast(float, row_bcast<at % 16>(w[at / 16]));
+  return __builtin_bit_cast(float, row_bcast<at % 16>(__builtin_bit_cast(uint32_t, w[at / 16])));
 }
 
-// MXFP4: scale of position 8g + J for the lane's V values (block c / (512/D)),
-// as a float32 whose exponent is the e8m0 byte (v_cvt_scalef32 reads the
-// exponent only: 0 is 2^-127, 255 gives NaN).
+// MXFP4: scale byte of position 8g + J for the lane's V values (block c /
+// (512/D)); lane c % 8 = J of the row holds the position's bytes.
 template <int D, int J>
 __device__ __forceinline__ uint32_t mx_vbyte(const uint32_t *w, int c) {
   const int blk = c / (512 / D);
@@ -264,6 +273,10 @@ __device__ __forceinline__ uint32_t mx_vbyte(const uint32_t *w, int c) {
   }
   return (x >> ((blk & 3) * 8)) & 0xffu;
 }
+
+// The float32 that v_cvt_scalef32 takes an e8m0 byte from: it reads the
+// exponent only, 0 being 2^-127 and 255 giving NaN.
+__device__ __forceinline__ float e8m0_scale(uint32_t byte) { return __builtin_bit_cast(float, byte << 23); }
 
 template <int I, int N, class F>
 __device__ __forceinline__ void static_for(F &&f) {
@@ -283,33 +296,59 @@ struct AttnWave {
   int qpos[NQ];                                              // position of the lane's query row
 };
 
-__device__ __forceinline__ float e8m0_scale(uint32_t byte) { return __builtin_bit_cast(float, byte << 23); }
-
+// One tile from its slot sl. bad: the lane's positions 8g..8g+7 lie on no page.
 template <int FMT, int D, int NQ, bool MASKED>
-__device__ __forceinline__ void attn_tile(AttnWave<FMT, D, NQ> &w, AttnTile<FMT, D> &x, const KvAttnArgs &a,
+__device__ __forceinline__ void attn_tile(AttnWave<FMT, D, NQ> &w, const uint8_t *sl, bool bad, const KvAttnArgs &a,
                                           const uint32_t *lut, int t, int lane) {
+  typedef AttnSlot<FMT, D> T;
   constexpr bool MX = FMT == GNF4_MXFP4;
   constexpr int KS = D / 32, ND = D / 16;
   const int c = lane & 15, g = lane >> 4;
   const uint32_t lane4 = (uint32_t)lane * 4;
   float s[NQ][8];
-  if constexpr (!MX) {                                       // absmax over the operand codebook's scale
+  const uint8_t *sc_k = sl + T::SOFF, *sc_v = sc_k + T::SC;
+  float ksn[2], vsn[2];                                      // NF4: absmax over the operand codebook's scale
+  if constexpr (!MX) {
 #pragma unroll
-    for (int i = 0; i < AttnTile<FMT, D>::SW; ++i) {
-      x.ks[i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, x.ks[i]) * kNF4InvScale);
-      x.vs[i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, x.vs[i]) * kNF4InvScale);
+    for (int i = 0; i < (D == 256 ? 2 : 1); ++i) {
+      const int at = g * (D / 8) + (D == 64 ? c & 7 : c) + 16 * i;
+      ksn[i] = reinterpret_cast<const float *>(sc_k)[at] * kNF4InvScale;
+      vsn[i] = reinterpret_cast<const float *>(sc_v)[at] * kNF4InvScale;
     }
   }
   // ---- scores of positions 8g..8g+7 for the lane's query row
   static_for<0, 2>([&](auto I) {
     constexpr int i = I;
     f32x4_t acc[NQ], blk[NQ];
+    uint32_t kc[KS];                                         // the lane's codes of its row of this K tile
+    uint32_t kb = 0;                                         // MXFP4: its scale byte(s)
+    const int tok = (c >> 2) * 8 + i * 4 + (c & 3);
+    if constexpr (MX && D == 128) {
+      const uint4 v = *reinterpret_cast<const uint4 *>(sl + i * 1024 + lane * 16);
+      kc[0] = v.x, kc[1] = v.y, kc[2] = v.z, kc[3] = v.w;
+      kb = sc_k[tok * 4 + g];
+    } else if constexpr (MX && D == 256) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(sl + ((i * 8 + 2 * g + e) * 16 + c) * 16);
+        kc[4 * e] = v.x, kc[4 * e + 1] = v.y, kc[4 * e + 2] = v.z, kc[4 * e + 3] = v.w;
+      }
+      kb = *reinterpret_cast<const uint16_t *>(sc_k + tok * 8 + 2 * g);
+    } else {
+      // MXFP4, D = 64: 8 bytes at g * 8 of the row; NF4: at b * 32 + g * 8 of block b
+#pragma unroll
+      for (int b = 0; b < D / 64; ++b) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(sl + ((i * T::CH + 2 * b + (g >> 1)) * 16 + c) * 16 + (g & 1) * 8);
+        kc[2 * b] = v.x, kc[2 * b + 1] = v.y;
+      }
+      if constexpr (MX) kb = sc_k[tok * 2 + (g >> 1)];
+    }
     static_for<0, KS>([&](auto K) {
       constexpr int k = K;
       bf16x8_t ka;
-      const uint32_t kw = x.kc[i][k];
+      const uint32_t kw = kc[k];
       if constexpr (MX) {
-        const float sc = e8m0_scale(D == 256 ? (k < KS / 2 ? x.ks[i] & 0xffu : x.ks[i] >> 8) : x.ks[i]);
+        const float sc = e8m0_scale(D == 256 ? (k < KS / 2 ? kb & 0xffu : kb >> 8) : kb);
         ka = op8(fp4_pair<0>(kw, sc), fp4_pair<1>(kw, sc), fp4_pair<2>(kw, sc), fp4_pair<3>(kw, sc));
       } else {
         ka = op8(lut_read(lut, lut_addr(kw, lane4, 0)), lut_read(lut, lut_addr(kw, lane4, 1)),
@@ -326,7 +365,7 @@ __device__ __forceinline__ void attn_tile(AttnWave<FMT, D, NQ> &w, AttnTile<FMT,
       if constexpr (!MX && (k & 1)) {                        // a block of 64 is complete
         static_for<0, 4>([&](auto J) {
           constexpr int j = J;
-          const float ab = nf4_absmax<D, 4 * i + j, k / 2>(x.ks);
+          const float ab = nf4_absmax<D, 4 * i + j, k / 2>(ksn);
 #pragma unroll
           for (int n = 0; n < NQ; ++n) acc[n][j] = k == 1 ? blk[n][j] * ab : fmaf(blk[n][j], ab, acc[n][j]);
         });
@@ -348,7 +387,7 @@ __device__ __forceinline__ void attn_tile(AttnWave<FMT, D, NQ> &w, AttnTile<FMT,
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int pos = t + g * 8 + j;
-        const bool ok = pos <= w.qpos[n] && pos >= lo && !x.bad;
+        const bool ok = pos <= w.qpos[n] && pos >= lo && !bad;
         see[n] |= ok ? 1u << j : 0u;
         s[n][j] = ok ? s[n][j] : kNegInf;
       }
@@ -382,8 +421,15 @@ __device__ __forceinline__ void attn_tile(AttnWave<FMT, D, NQ> &w, AttnTile<FMT,
   }
   // ---- O^T += V^T P^T
   if constexpr (MX) {
-    uint32_t sb[8];
-    static_for<0, 8>([&](auto J) { sb[J] = mx_vbyte<D, J>(x.vs, c); });
+    uint32_t sb[8], vw[2] = {0, 0};
+    const int vt = g * 8 + (c & 7);
+    if constexpr (D == 64) vw[0] = *reinterpret_cast<const uint16_t *>(sc_v + vt * 2);
+    else if constexpr (D == 128) vw[0] = *reinterpret_cast<const uint32_t *>(sc_v + vt * 4);
+    else {
+      const uint2 v = *reinterpret_cast<const uint2 *>(sc_v + vt * 8);
+      vw[0] = v.x, vw[1] = v.y;
+    }
+    static_for<0, 8>([&](auto J) { sb[J] = mx_vbyte<D, J>(vw, c); });
     if constexpr (MASKED) {
       // A NaN scale in a place that some row does not see: 0 * NaN must not
       // reach that row. Such values are taken out of the product and their NaN
@@ -415,13 +461,24 @@ __device__ __forceinline__ void attn_tile(AttnWave<FMT, D, NQ> &w, AttnTile<FMT,
     float sc[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) sc[j] = e8m0_scale(sb[j]);
+    uint32_t vc[8][D == 256 ? 2 : 1];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint8_t *row = sl + T::VOFF + (4 * j + g) * (D / 2) + c * (D / 32);
+      if constexpr (D == 64) vc[j][0] = *reinterpret_cast<const uint16_t *>(row);
+      else if constexpr (D == 128) vc[j][0] = *reinterpret_cast<const uint32_t *>(row);
+      else {
+        const uint2 v = *reinterpret_cast<const uint2 *>(row);
+        vc[j][0] = v.x, vc[j][1] = v.y;
+      }
+    }
     // byte y of a lane's codes holds its values 2y and 2y+1
 #pragma unroll
     for (int y = 0; y < ND / 2; ++y) {
       uint32_t pr[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const uint32_t cw = x.vc[j][y >> 2];
+        const uint32_t cw = vc[j][y >> 2];
         pr[j] = (y & 3) == 0 ? fp4_pair<0>(cw, sc[j]) : (y & 3) == 1 ? fp4_pair<1>(cw, sc[j])
               : (y & 3) == 2 ? fp4_pair<2>(cw, sc[j]) : fp4_pair<3>(cw, sc[j]);
       }
@@ -443,7 +500,11 @@ __device__ __forceinline__ void attn_tile(AttnWave<FMT, D, NQ> &w, AttnTile<FMT,
     static_for<0, D / 64>([&](auto BL) {
       constexpr int b = BL;
       float ab[8];
-      static_for<0, 8>([&](auto J) { ab[J] = nf4_absmax<D, J, b>(x.vs); });
+      uint32_t vc[8];                                        // lane c: values 4c .. 4c + 3 of the block
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        vc[j] = *reinterpret_cast<const uint16_t *>(sl + T::VOFF + (4 * j + g) * (D / 2) + b * 32 + c * 2);
+      static_for<0, 8>([&](auto J) { ab[J] = nf4_absmax<D, J, b>(vsn); });
       bf16x8_t pq[NQ];
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
@@ -459,7 +520,7 @@ __device__ __forceinline__ void attn_tile(AttnWave<FMT, D, NQ> &w, AttnTile<FMT,
       for (int y = 0; y < 2; ++y) {
         uint32_t pr[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) pr[j] = lut_read(lut, lut_addr(x.vc[j][b], lane4, y));
+        for (int j = 0; j < 8; ++j) pr[j] = lut_read(lut, lut_addr(vc[j], lane4, y));
         uint32_t e[4], f[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -501,124 +562,70 @@ __device__ __forceinline__ AttnScale attn_finish(float m, float l, const float *
   return r;
 }
 
-// Shares of the numbered rounds: workgroup w takes [w * share, (w + 1) * share).
-__device__ __forceinline__ int64_t attn_share(int64_t total) { return (total + kAttnGroups - 1) / kAttnGroups; }
+// Shares of the numbered runs: workgroup w takes [w * share, (w + 1) * share).
+__device__ __forceinline__ int attn_share(int total) { return (total + kAttnGroups - 1) / kAttnGroups; }
 
-// Sum over the workgroup of one value per thread, in every thread.
-__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t *lds, int tid, int waves) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
-  __syncthreads();
-  if ((tid & 63) == 0) lds[tid >> 6] = v;
-  __syncthreads();
-  v = 0;
-  for (int i = 0; i < waves; ++i) v += lds[i];
-  return v;
-}
-
-template <int FMT, int D, int NQ, int NW>
-__global__ __launch_bounds__(64 * NW, NW / 4) void kv_attn_kernel(KvAttnArgs a) {
+template <int FMT, int D, int NQ, int NW, int S>
+__global__ __launch_bounds__(64 * NW, NW == 4 ? (NQ == 1 && D <= 128 ? 4 : 1) : NW / 4) void kv_attn_kernel(KvAttnArgs a) {
+  typedef AttnSlot<FMT, D> T;
   constexpr bool MX = FMT == GNF4_MXFP4;
   constexpr int NT = 64 * NW, ROUND = 32 * NW;
   constexpr int KS = D / 32, ND = D / 16, M = 16 * NQ;
-  constexpr int DC = D < 128 ? D : 128;                      // values of a row joined at a time
-  constexpr int LUT = MX ? 0 : kLutWords;
-  constexpr int DEPTH = D == 256 || NQ > 1 || (!MX && D == 128) ? 2 : 3;          // tiles in registers: one computed, the others in flight
   // one block, so that the table starts at LDS address 0 and a byte's address
   // is what lut_addr forms
   struct Lds {
-    uint32_t lut[LUT ? LUT : 4];
-    float red[NW * 16 * (DC + 4)];
+    uint32_t lut[MX ? 4 : kLutWords];
+    union {
+      uint8_t ring[NW * S * T::BYTES];                       // S slots of every wave
+      float red[NW * 16 * (D + 4)];                          // the waves' O tile, when they join
+    };
     float sm[NW][M], sl[NW][M];
-    int64_t pre[NT + 1], wsum[NW];
   };
   __shared__ __attribute__((aligned(16))) Lds lds;
-  uint32_t *lut = lds.lut;
-  float *red = lds.red;
-  auto &sm = lds.sm, &sl = lds.sl;
-  int64_t *pre = lds.pre, *wsum = lds.wsum;
   const KvView &kv = a.kv;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = lane & 15, g = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const uint8_t *ring = lds.ring + wave * S * T::BYTES;
+  const uint32_t ring_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)ring;
   const int Hq = kv.H * a.G;
   if constexpr (!MX) {
-    fill_nf4_lut<NT>(lut, tid);
+    fill_nf4_lut<NT>(lds.lut, tid);
     __syncthreads();
   }
 
-  // ---- the run of rounds: [u, end), from sequence b0 + (an index into pre) on
-  int64_t u = 0, end = 0, base = 0;                          // base: rounds before the sequences of pre
-  int b = 0, b0 = 0;
+  // ---- the share [u, end) of the runs, by every wave for itself
+  int u = 0, end = 0, b0 = 0, base = 0;                      // base: runs before sequence b0
+  int sum = 0;
   if (a.shared) {
-    int64_t v = tid < kv.B ? attn_units(a, tid, M, ROUND) : 0, total = v;
-    for (int i = tid + NT; i < kv.B; i += NT) total += attn_units(a, i, M, ROUND);
-    total = block_sum(total, wsum, tid, NW);
-    const int64_t share = attn_share(total);
+    sum = attn_sums(a, 0, M, lane);
+    int total = __builtin_amdgcn_readlane(sum, 63);
+    for (int i = 64; i < kv.B; i += 64) total += __builtin_amdgcn_readlane(attn_sums(a, i, M, lane), 63);
+    const int share = attn_share(total);
     u = blockIdx.x * share;
     end = min(total, u + share);
-    if (u >= end) return;
-    for (;;) {                                               // the chunk of sequences that holds round u
-      int64_t s = v;
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const int64_t o = __shfl_up(s, d, 64);
-        if (lane >= d) s += o;
-      }
-      __syncthreads();
-      if (lane == 63) wsum[wave] = s;
-      __syncthreads();
-      int64_t before = base;
-      for (int i = 0; i < wave; ++i) before += wsum[i];
-      pre[tid + 1] = before + s;
-      if (tid == 0) pre[0] = base;
-      __syncthreads();
-      if (u < pre[NT] || b0 + NT >= kv.B) break;
-      base = pre[NT];
-      b0 += NT;
-      v = b0 + tid < kv.B ? attn_units(a, b0 + tid, M, ROUND) : 0;
-    }
-    for (int lo = 0, n = NT; n > 1;) {             // the last sequence with pre <= u: 64 probes at a time
-      const int step = (n + 63) >> 6;
-      const bool below = lane * step < n && pre[lo + lane * step] <= u;
-      const int k = __popcll(__ballot(below));
-      lo += (k - 1) * step;
-      n = min(step, n - (k - 1) * step);
-      b = lo;
-    }
   }
 
   for (;;) {
-    // ---- the next problem: tile mt, head h of sequence bb; its rounds [q0, q1)
+    // ---- the next problem: tile mt, head h of sequence bb; its runs [q0, q1)
     int bb, mt, h, q0 = 0, q1;
     AttnSeq x;
     if (a.shared) {
       if (u >= end) return;
-      while (u >= pre[b + 1]) {                              // sequences without rows have no rounds
-        if (++b < NT) continue;
-        base = pre[NT];
-        b0 += NT;
-        b = 0;
-        int64_t s = b0 + tid < kv.B ? attn_units(a, b0 + tid, M, ROUND) : 0;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-          const int64_t o = __shfl_up(s, d, 64);
-          if (lane >= d) s += o;
-        }
-        __syncthreads();
-        if (lane == 63) wsum[wave] = s;
-        __syncthreads();
-        int64_t before = base;
-        for (int i = 0; i < wave; ++i) before += wsum[i];
-        pre[tid + 1] = before + s;
-        if (tid == 0) pre[0] = base;
-        __syncthreads();
+      uint64_t past;
+      while ((past = __ballot(base + sum > u)) == 0) {       // sequences without rows have no runs
+        base += __builtin_amdgcn_readlane(sum, 63);
+        b0 += 64;
+        sum = attn_sums(a, b0, M, lane);
       }
-      bb = b0 + b;
-      x = attn_seq(a, bb, M, ROUND);
-      const int64_t rel = u - pre[b], item = rel / x.units;
-      q0 = (int)(rel - item * x.units);
-      mt = (int)(item / kv.H);
-      h = (int)(item - (int64_t)mt * kv.H);
-      q1 = (int)min((int64_t)x.units, q0 + (end - u));
+      const int l = __builtin_ctzll(past);
+      bb = b0 + l;
+      x = attn_seq(a, bb, M);
+      const int rel = u - (base + __builtin_amdgcn_readlane(sum, l) - attn_units(a, x));
+      const int item = rel / x.units;
+      q0 = rel - item * x.units;
+      mt = item / kv.H;
+      h = item - mt * kv.H;
+      q1 = min(x.units, q0 + (end - u));
       u += q1 - q0;
     } else {
       int idx = (int)blockIdx.x;
@@ -626,13 +633,24 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void kv_attn_kernel(KvAttnArgs a) 
       idx /= kv.H;
       mt = idx % a.n_mt;
       bb = idx / a.n_mt;
-      x = attn_seq(a, bb, M, ROUND);
+      x = attn_seq(a, bb, M);
       if (mt >= x.mts) return;
       q1 = x.units;
     }
     const bool whole = q0 == 0 && q1 == x.units;
-    const int t0 = x.lo + q0 * ROUND, t1 = min(x.hi, x.lo + q1 * ROUND), row0 = mt * M;
+    const int t0 = x.lo + q0 * kAttnUnit, row0 = mt * M;
+    const int t1 = q1 == x.units ? x.hi : x.lo + q1 * kAttnUnit;
 
+    // ---- S - 1 tiles under way, then the queries
+    const int first = t0 + wave * 32, tiles = first < t1 ? (t1 - first + ROUND - 1) / ROUND : 0;
+    uint32_t bad = 0;                                        // two bits per slot
+    AttnPages pg = attn_pages(kv, bb, first);
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i)
+      if (i < tiles) {
+        bad |= attn_send<FMT, D>(kv, h, first + i * ROUND, pg, ring_at + i * T::BYTES, lane) << (2 * i);
+        pg = attn_pages(kv, bb, first + (i + 1) * ROUND);
+      }
     AttnWave<FMT, D, NQ> w;
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
@@ -643,15 +661,15 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void kv_attn_kernel(KvAttnArgs a) 
       w.l[n] = 0.0f;
       const uint16_t *qp = a.q + (int64_t)(x.r0 + tok) * a.q_stride + (int64_t)(h * a.G + row - tok * a.G) * D;
 #pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        const int d = MX ? g * (D / 4) + k * 8 : (k >> 1) * 64 + g * 16 + (k & 1) * 8;
+      for (int i = 0; i < KS; ++i) {
+        const int d = MX ? g * (D / 4) + i * 8 : (i >> 1) * 64 + g * 16 + (i & 1) * 8;
         uint4 v = make_uint4(0, 0, 0, 0);
         if (ok) v = *reinterpret_cast<const uint4 *>(qp + d);
         v.x ^= a.q_sign;
         v.y ^= a.q_sign;
         v.z ^= a.q_sign;
         v.w ^= a.q_sign;
-        w.q[n][k] = __builtin_bit_cast(bf16x8_t, v);
+        w.q[n][i] = __builtin_bit_cast(bf16x8_t, v);
       }
 #pragma unroll
       for (int d = 0; d < ND; ++d) w.o[n][d] = f32x4_t{0, 0, 0, 0};
@@ -659,33 +677,36 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void kv_attn_kernel(KvAttnArgs a) 
     const int last = min(row0 + M, x.rows) - 1;
     const int full_hi = x.start + row0 / a.G;                // every row sees from full_lo to full_hi
     const int full_lo = a.window > 0 ? x.start + last / a.G - a.window + 1 : 0;
-    AttnTile<FMT, D> tl[DEPTH];
-    AttnPages pg[DEPTH];
-    int t = t0 + wave * 32;
-    if (t < t1) {
-      // DEPTH - 1 rounds ahead the codes are in flight, one more the page ids
+    // The queries are here before the loop: a wait for them inside it would be
+    // one for the tiles under way as well.
 #pragma unroll
-      for (int i = 0; i < DEPTH; ++i) pg[i] = attn_pages(kv, bb, t + i * ROUND);
+    for (int n = 0; n < NQ; ++n)
 #pragma unroll
-      for (int i = 0; i < DEPTH - 1; ++i)
-        if (t + i * ROUND < t1) attn_load<FMT, D>(tl[i], kv, h, t + i * ROUND, pg[i], lane);
-      for (bool more = true; more;) {
-#pragma unroll
-        for (int i = 0; i < DEPTH; ++i) {
-          constexpr int A = DEPTH - 1;
-          pg[i] = attn_pages(kv, bb, t + DEPTH * ROUND);
-          if (t + A * ROUND < t1)
-            attn_load<FMT, D>(tl[(i + A) % DEPTH], kv, h, t + A * ROUND, pg[(i + A) % DEPTH], lane);
-          const bool all = t >= full_lo && t + 31 <= full_hi && __ballot(tl[i].bad) == 0;
-          if (all) attn_tile<FMT, D, NQ, false>(w, tl[i], a, lut, t, lane);
-          else attn_tile<FMT, D, NQ, true>(w, tl[i], a, lut, t, lane);
-          t += ROUND;
-          if (t >= t1) {
-            more = false;
-            break;
-          }
-        }
+      for (int i = 0; i < KS; ++i) asm volatile("" : "+v"(w.q[n][i]));
+
+    int slot = 0, next = S - 1;                              // of this tile, of the one sent now
+    for (int i = 0; i < tiles; ++i) {
+      const int t = first + i * ROUND;
+      if (i + S - 1 < tiles) {
+        bad &= ~(3u << (2 * next));
+        bad |= attn_send<FMT, D>(kv, h, t + (S - 1) * ROUND, pg, ring_at + next * T::BYTES, lane) << (2 * next);
+        pg = attn_pages(kv, bb, t + S * ROUND);
+        wait_vm<(S - 1) * T::LOADS>();
+      } else if (S > 3 && i + 2 < tiles) {
+        wait_vm<2 * T::LOADS>();
+      } else if (S > 2 && i + 1 < tiles) {
+        wait_vm<T::LOADS>();
+      } else {
+        wait_vm<0>();
       }
+      const uint32_t bd = (bad >> (2 * slot)) & 3u;
+      const uint8_t *sl = ring + slot * T::BYTES;
+      if (t >= full_lo && t + 31 <= full_hi && bd == 0)
+        attn_tile<FMT, D, NQ, false>(w, sl, false, a, lds.lut, t, lane);
+      else
+        attn_tile<FMT, D, NQ, true>(w, sl, ((bd >> (lane >> 5)) & 1u) != 0, a, lds.lut, t, lane);
+      slot = slot + 1 == S ? 0 : slot + 1;
+      next = next + 1 == S ? 0 : next + 1;
     }
 
     // ---- join the waves
@@ -693,106 +714,98 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void kv_attn_kernel(KvAttnArgs a) 
     for (int n = 0; n < NQ; ++n) {
       w.l[n] = sum_xor16_32(w.l[n]);
       if (g == 0) {
-        sm[wave][n * 16 + c] = w.m[n];
-        sl[wave][n * 16 + c] = w.l[n];
+        lds.sm[wave][n * 16 + c] = w.m[n];
+        lds.sl[wave][n * 16 + c] = w.l[n];
       }
     }
-    __syncthreads();
+    __syncthreads();                                         // all tiles are read: their slots become red
     // a problem that goes on from the workgroup before lies in this one's first
-    // slot, one that goes on in the next in its second
-    const int64_t slot = 2 * (int64_t)blockIdx.x + (q0 == 0 ? 1 : 0);
+    // slot of the partial results, one that goes on in the next in its second
+    const int64_t part = 2 * (int64_t)blockIdx.x + (q0 == 0 ? 1 : 0);
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
       const int r = n * 16 + c;
-      float top = sm[0][r];
+      float top = lds.sm[0][r];
 #pragma unroll
-      for (int v = 1; v < NW; ++v) top = fmaxf(top, sm[v][r]);
+      for (int v = 1; v < NW; ++v) top = fmaxf(top, lds.sm[v][r]);
       const float f = __builtin_amdgcn_exp2f(w.m[n] - (top == kNegInf ? 0.0f : top));
+      float *mine = lds.red + (wave * 16 + c) * (D + 4);
 #pragma unroll
-      for (int dc = 0; dc < D; dc += DC) {
-        float *mine = red + (wave * 16 + c) * (DC + 4);
+      for (int d = 0; d < ND; ++d)
 #pragma unroll
-        for (int d = 0; d < ND; ++d)
+        for (int i = 0; i < 4; ++i) {
+          const int cc = g * 4 + i;
+          mine[MX ? cc * (D / 16) + d : (d >> 2) * 64 + cc * 4 + (d & 3)] = w.o[n][d][i] * f;
+        }
+      __syncthreads();
+      for (int k4 = tid; k4 < 16 * (D / 4); k4 += NT) {
+        const int rr = k4 / (D / 4), d4 = (k4 - rr * (D / 4)) * 4;
+        const int kr = n * 16 + rr, row = row0 + kr;
+        if (row < x.rows) {
+          float4 s = make_float4(0, 0, 0, 0);
+          float mr = lds.sm[0][kr], l = 0.0f;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int cc = g * 4 + i;
-            const int at = MX ? cc * (D / 16) + d : (d >> 2) * 64 + cc * 4 + (d & 3);
-            if (at >= dc && at < dc + DC) mine[at - dc] = w.o[n][d][i] * f;
+          for (int v = 0; v < NW; ++v) {
+            const float4 o = *reinterpret_cast<const float4 *>(lds.red + (v * 16 + rr) * (D + 4) + d4);
+            s.x += o.x;
+            s.y += o.y;
+            s.z += o.z;
+            s.w += o.w;
+            mr = fmaxf(mr, lds.sm[v][kr]);
           }
-        __syncthreads();
-        for (int k4 = tid; k4 < 16 * (DC / 4); k4 += NT) {
-          const int rr = k4 / (DC / 4), d4 = (k4 - rr * (DC / 4)) * 4;
-          const int k = n * 16 + rr, row = row0 + k;
-          if (row < x.rows) {
-            float4 s = make_float4(0, 0, 0, 0);
-            float mr = sm[0][k], l = 0.0f;
+          const float mrs = mr == kNegInf ? 0.0f : mr;
 #pragma unroll
-            for (int v = 0; v < NW; ++v) {
-              const float4 o = *reinterpret_cast<const float4 *>(red + (v * 16 + rr) * (DC + 4) + d4);
-              s.x += o.x;
-              s.y += o.y;
-              s.z += o.z;
-              s.w += o.w;
-              mr = fmaxf(mr, sm[v][k]);
-            }
-            const float mrs = mr == kNegInf ? 0.0f : mr;
-#pragma unroll
-            for (int v = 0; v < NW; ++v) l += sl[v][k] * __builtin_amdgcn_exp2f(sm[v][k] - mrs);
-            if (whole) {
-              const int tok = row / a.G, hq = h * a.G + row - tok * a.G;
-              const AttnScale z = attn_finish(mr, l, a.sinks, hq);
-              *reinterpret_cast<uint2 *>(a.out + (int64_t)(x.r0 + tok) * a.out_stride + (int64_t)hq * D + dc + d4) =
-                  make_uint2(pk_bf16(s.x * z.mul, s.y * z.mul), pk_bf16(s.z * z.mul, s.w * z.mul));
-              if (a.lse && dc + d4 == 0) a.lse[(int64_t)(x.r0 + tok) * Hq + hq] = z.lse;
-            } else {
-              const int64_t pr = slot * M + k;
-              *reinterpret_cast<float4 *>(a.part + pr * D + dc + d4) = s;
-              if (dc + d4 == 0)
-                *reinterpret_cast<float2 *>(a.part + 2LL * kAttnGroups * M * D + pr * 2) = make_float2(mr, l);
-            }
+          for (int v = 0; v < NW; ++v) l += lds.sl[v][kr] * __builtin_amdgcn_exp2f(lds.sm[v][kr] - mrs);
+          if (whole) {
+            const int tok = row / a.G, hq = h * a.G + row - tok * a.G;
+            const AttnScale z = attn_finish(mr, l, a.sinks, hq);
+            *reinterpret_cast<uint2 *>(a.out + (int64_t)(x.r0 + tok) * a.out_stride + (int64_t)hq * D + d4) =
+                make_uint2(pk_bf16(s.x * z.mul, s.y * z.mul), pk_bf16(s.z * z.mul, s.w * z.mul));
+            if (a.lse && d4 == 0) a.lse[(int64_t)(x.r0 + tok) * Hq + hq] = z.lse;
+          } else {
+            const int64_t pr = part * M + kr;
+            *reinterpret_cast<float4 *>(a.part + pr * D + d4) = s;
+            if (d4 == 0) *reinterpret_cast<float2 *>(a.part + 2LL * kAttnGroups * M * D + pr * 2) = make_float2(mr, l);
           }
         }
-        __syncthreads();
       }
+      __syncthreads();
     }
     if (!a.shared) return;
   }
 }
 
-// Puts together the problems that lie in several runs: a workgroup per problem,
+// Puts together the problems that lie in several shares: a workgroup per problem,
 // a thread per four values of a row.
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 512;
 
 template <int D>
-__global__ __launch_bounds__(kJoinThreads) void kv_attn_join_kernel(KvAttnArgs a, int M, int round) {
-  __shared__ int64_t wsum[kJoinThreads / 64];
+__global__ __launch_bounds__(kJoinThreads) void kv_attn_join_kernel(KvAttnArgs a, int M) {
   const KvView &kv = a.kv;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 63;
   int idx = (int)blockIdx.x;
   const int h = idx % kv.H;
   idx /= kv.H;
   const int mt = idx % a.n_mt, b = idx / a.n_mt;
-  const AttnSeq x = attn_seq(a, b, M, round);
-  int64_t first = 0, total = 0;
-  for (int i = tid; i < kv.B; i += kJoinThreads) {
-    const int64_t n = attn_units(a, i, M, round);
-    total += n;
-    first += i < b ? n : 0;
+  const AttnSeq x = attn_seq(a, b, M);
+  int first = 0, total = 0;
+  for (int i = 0; i < kv.B; i += 64) {
+    const int sum = attn_sums(a, i, M, lane);
+    if (b >= i && b < i + 64) first = total + __builtin_amdgcn_readlane(sum, b - i) - attn_units(a, x);
+    total += __builtin_amdgcn_readlane(sum, 63);
   }
-  total = block_sum(total, wsum, tid, kJoinThreads / 64);
-  first = block_sum(first, wsum, tid, kJoinThreads / 64);
   if (mt >= x.mts) return;
-  const int64_t share = attn_share(total);
-  first += ((int64_t)mt * kv.H + h) * x.units;
-  const int64_t w0 = first / share, w1 = (first + x.units - 1) / share;
+  const int share = attn_share(total);
+  first += (mt * kv.H + h) * x.units;
+  const int w0 = first / share, w1 = (first + x.units - 1) / share;
   if (w0 == w1) return;                                      // written by its only workgroup
-  const int n = (int)(w1 - w0) + 1;
+  const int n = w1 - w0 + 1;
   const float2 *ml = reinterpret_cast<const float2 *>(a.part + 2LL * kAttnGroups * M * D);
   for (int u = tid; u < M * (D / 4); u += kJoinThreads) {
     const int r = u / (D / 4), d4 = (u - r * (D / 4)) * 4, row = mt * M + r;
     if (row >= x.rows) break;
     // the first workgroup's second slot, the first slots of the others
-    auto at = [&](int s) { return (2 * (w0 + s) + (s == 0 ? 1 : 0)) * M + r; };
+    auto at = [&](int s) { return (int64_t)(2 * (w0 + s) + (s == 0 ? 1 : 0)) * M + r; };
     float top = kNegInf, l = 0.0f;
     float4 o = make_float4(0, 0, 0, 0);
 #pragma unroll 4
@@ -817,15 +830,23 @@ __global__ __launch_bounds__(kJoinThreads) void kv_attn_join_kernel(KvAttnArgs a
   }
 }
 
-// Rows per tile from the most new tokens of a sequence. Short contexts, of up
-// to four rounds, take a workgroup per problem and one launch; where these are
-// at least as many as compute units, of four waves, so that two fit on one.
+// Waves and slots of a workgroup that has a compute unit to itself, by what the
+// registers (four waves per SIMD have 128 each, two 256) and the LDS (160 KB,
+// 64 of them the NF4 table) hold.
+template <int FMT, int D, int NQ>
+struct AttnCfg {
+  static constexpr bool MX = FMT == GNF4_MXFP4;
+  static constexpr int NW = NQ == 1 && D == 64 ? 16 : D == 256 && !MX ? 4 : 8;
+  static constexpr int S = NW == 8 && MX && D == 128 ? 3 : 2;
+};
+
+// Rows per tile from the most new tokens of a sequence. Short contexts take a
+// workgroup per problem and one launch; where these are at least as many as
+// compute units, of four waves, so that several fit on one.
 bool kv_attention_plan(int32_t D, int32_t H, int32_t G, int32_t B, int64_t n_tokens, int32_t max_new,
-                       int64_t max_len, int32_t window, KvAttnPlan *p) {
+                       int64_t max_len, int64_t capacity, int32_t window, KvAttnPlan *p) {
   const int64_t rows = (int64_t)max_new * G;
   p->nq = rows <= 16 || D == 256 ? 1 : 2;                     // D = 256: the registers hold no second tile
-  p->waves = p->nq == 1 && D <= 128 ? 8 : 4;
-  int round = 32 * p->waves;
   const int M = 16 * p->nq;
   const int64_t n_mt = (rows + M - 1) / M;
   p->items = (int64_t)B * n_mt * H;
@@ -833,29 +854,31 @@ bool kv_attention_plan(int32_t D, int32_t H, int32_t G, int32_t B, int64_t n_tok
   if (window > 0) len = std::min<int64_t>(len, (int64_t)window + max_new - 1 + 31);
   if (p->items > 0x7fffffffLL) return false;
   p->n_mt = (int32_t)n_mt;
-  p->shared = len > 4 * round;
-  if (!p->shared && p->items >= kAttnGroups) p->waves = 4;
+  p->shared = len > 1024;
+  p->small = !p->shared && p->items >= kAttnGroups;
+  // the runs are counted in 32 bits
+  if (p->shared && p->items * ((capacity + kAttnUnit - 1) / kAttnUnit) > 0x7fffffffLL) p->shared = 0;
   p->bytes = p->shared ? (size_t)(2 * kAttnGroups * M) * (D + 2) * 4 : 0;
   return true;
 }
 
-template <int FMT, int D, int NQ, int NW>
+template <int FMT, int D, int NQ, int NW, int S>
 static hipError_t attn_go(const KvAttnArgs &a, const KvAttnPlan &p, hipStream_t s) {
-  hipLaunchKernelGGL((kv_attn_kernel<FMT, D, NQ, NW>), dim3(p.shared ? kAttnGroups : (unsigned)p.items), dim3(64 * NW),
+  hipLaunchKernelGGL((kv_attn_kernel<FMT, D, NQ, NW, S>), dim3(p.shared ? kAttnGroups : (unsigned)p.items), dim3(64 * NW),
                      0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !p.shared) return e;
-  hipLaunchKernelGGL((kv_attn_join_kernel<D>), dim3((unsigned)p.items), dim3(kJoinThreads), 0, s, a, 16 * NQ, 32 * NW);
+  hipLaunchKernelGGL((kv_attn_join_kernel<D>), dim3((unsigned)p.items), dim3(kJoinThreads), 0, s, a, 16 * NQ);
   return hipGetLastError();
 }
 
 template <int FMT, int D>
 static hipError_t attn_nq(const KvAttnArgs &a, const KvAttnPlan &p, hipStream_t s) {
   if constexpr (D <= 128) {
-    if (p.nq == 2) return attn_go<FMT, D, 2, 4>(a, p, s);
-    if (p.waves == 8) return attn_go<FMT, D, 1, 8>(a, p, s);
+    if (p.nq == 2) return attn_go<FMT, D, 2, AttnCfg<FMT, D, 2>::NW, AttnCfg<FMT, D, 2>::S>(a, p, s);
   }
-  return attn_go<FMT, D, 1, 4>(a, p, s);
+  if (p.small) return attn_go<FMT, D, 1, 4, 2>(a, p, s);
+  return attn_go<FMT, D, 1, AttnCfg<FMT, D, 1>::NW, AttnCfg<FMT, D, 1>::S>(a, p, s);
 }
 
 hipError_t launch_kv_attention(const KvAttnArgs &args, const KvAttnPlan &p, int32_t format, hipStream_t s) {

@@ -42,12 +42,12 @@ struct KvAttnArgs {
 
 // How one call is cut (attention.hip).
 struct KvAttnPlan {
-  int32_t nq, waves, n_mt, shared;
+  int32_t nq, n_mt, shared, small;
   int64_t items;                  // sequences * n_mt * H
   size_t bytes;
 };
 bool kv_attention_plan(int32_t D, int32_t H, int32_t G, int32_t B, int64_t n_tokens, int32_t max_new,
-                       int64_t max_len, int32_t window, KvAttnPlan *p);
+                       int64_t max_len, int64_t capacity, int32_t window, KvAttnPlan *p);
 
 hipError_t launch_kv_write(const KvRowsArgs &a, int32_t format, hipStream_t s);
 hipError_t launch_kv_read(const KvRowsArgs &a, int32_t format, int32_t out_f32, hipStream_t s);
