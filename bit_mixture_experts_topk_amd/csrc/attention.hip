@@ -175,30 +175,33 @@ struct AttnSlot {
   static constexpr int LOADS = 2 * N16 + (SC == 256 ? 2 : 1);
 };
 
-// Page ids of a tile: of its first and last 16 positions (pages hold 16 at least).
-struct AttnPages {
+// Where one head's rows lie, and page ids of 64 tiles of the wave, one per lane:
+// of the first and the last 16 positions (pages hold 16 at least).
+struct AttnPlace {
+  const uint8_t *k, *v, *ks, *vs;                            // the head's rows on page 0
+  int32_t page_rows, page_shift, n_pages;                    // rows of a page, all heads
   int a, b;
 };
 
-__device__ __forceinline__ AttnPages attn_pages(const KvView &kv, int b, int t) {
-  const_ints row = (const_ints)(uintptr_t)(kv.pages + (int64_t)b * kv.max_pages);
-  AttnPages p;
-  p.a = row[min(t >> kv.page_shift, kv.max_pages - 1)];
-  p.b = row[min((t + 16) >> kv.page_shift, kv.max_pages - 1)];
-  return p;
+__device__ __forceinline__ void attn_pages(AttnPlace &x, const KvView &kv, int bb, int t) {
+  const int32_t *row = kv.pages + (int64_t)bb * kv.max_pages;
+  x.a = row[min(t >> kv.page_shift, kv.max_pages - 1)];
+  x.b = row[min((t + 16) >> kv.page_shift, kv.max_pages - 1)];
+  asm volatile("" : "+v"(x.a), "+v"(x.b));                   // here, not at their use among the tiles under way
 }
 
-// Sends the tile at position t into the slot at LDS address lds. Returns which
-// halves of it lie on no page (bit 0, 1): these read page 0 and are masked.
+// Sends the tile at position t (page ids in lane l of x) into the slot at LDS
+// address lds. Returns which halves of it lie on no page (bit 0, 1): these
+// read page 0 and are masked.
 template <int FMT, int D>
-__device__ __forceinline__ uint32_t attn_send(const KvView &kv, int h, int t, AttnPages p, uint32_t lds, int lane) {
+__device__ __forceinline__ uint32_t attn_send(const AttnPlace &x, int l, int t, uint32_t lds, int lane) {
   typedef AttnSlot<FMT, D> T;
   constexpr int RB = D / 2, SB = T::SC / 32;                 // bytes per row: codes, scales
-  const int mask = (1 << kv.page_shift) - 1;
-  const bool bada = (uint32_t)p.a >= (uint32_t)kv.n_pages, badb = (uint32_t)p.b >= (uint32_t)kv.n_pages;
-  const int pa = bada ? 0 : p.a, pb = badb ? 0 : p.b;
-  const int64_t ra = (((int64_t)pa * kv.H + h) << kv.page_shift) + (t & mask);
-  const uint8_t *ks = static_cast<const uint8_t *>(kv.k_scales), *vs = static_cast<const uint8_t *>(kv.v_scales);
+  int pa = __builtin_amdgcn_readlane(x.a, l), pb = __builtin_amdgcn_readlane(x.b, l);
+  const bool bada = (uint32_t)pa >= (uint32_t)x.n_pages, badb = (uint32_t)pb >= (uint32_t)x.n_pages;
+  pa = bada ? 0 : pa;
+  pb = badb ? 0 : pb;
+  const int64_t ra = (int64_t)pa * x.page_rows + (t & ((1 << x.page_shift) - 1));
   // K: LDS piece (i, q, r) = piece q of the row of tile i, lane r
   constexpr int LCH = T::CH == 2 ? 1 : T::CH == 4 ? 2 : 3;
   const int r = lane & 15;
@@ -212,8 +215,8 @@ __device__ __forceinline__ uint32_t attn_send(const KvView &kv, int h, int t, At
   constexpr int SW = T::SC == 512 ? 16 : 4;                  // bytes per lane
   constexpr int SL = T::SC / SW;                             // lanes per side
   const int sside = T::SC == 256 ? 0 : (lane / SL) & 1, soff = (T::SC == 256 ? lane : lane % SL) * SW;
-  if (kv.page_shift > 4) {
-    const uint8_t *kb = kv.k_codes + ra * RB, *vb = kv.v_codes + ra * RB;
+  if (x.page_shift > 4) {
+    const uint8_t *kb = x.k + ra * RB, *vb = x.v + ra * RB;
 #pragma unroll
     for (int n = 0; n < T::N16; ++n) {
       const int step = T::CH == 8 ? (n >> 1) * 4 * RB + (n & 1) * 64 : n * 4 * RB;
@@ -221,20 +224,20 @@ __device__ __forceinline__ uint32_t attn_send(const KvView &kv, int h, int t, At
       dma16(vb + n * VSTEP * RB, (uint32_t)(vtok * RB + vq * 16), lds + T::VOFF + n * 1024);
     }
     if constexpr (T::SC == 256) {
-      dma4(ks + ra * SB, (uint32_t)soff, lds + T::SOFF);
-      dma4(vs + ra * SB, (uint32_t)soff, lds + T::SOFF + 256);
+      dma4(x.ks + ra * SB, (uint32_t)soff, lds + T::SOFF);
+      dma4(x.vs + ra * SB, (uint32_t)soff, lds + T::SOFF + 256);
     } else {
-      const uint8_t *q = (sside ? vs : ks) + ra * SB + soff;
+      const uint8_t *q = (sside ? x.vs : x.ks) + ra * SB + soff;
       if constexpr (SW == 16) dma16(q, lds + T::SOFF);
       else dma4(q, lds + T::SOFF);
     }
   } else {
     // pages of 16: the second half of the tile lies on another one
-    const int64_t rb = ((int64_t)pb * kv.H + h) * 16 - 16;
+    const int64_t rb = (int64_t)pb * x.page_rows - 16;
     const int64_t rk = (r >> 2) < 2 ? ra : rb, rv = (vrow & 3) < 2 ? ra : rb;
     const int64_t rs = soff / SB < 16 ? ra : rb;
-    const uint8_t *kb = kv.k_codes + rk * RB + ktok * RB + kq * 16;
-    const uint8_t *vb = kv.v_codes + rv * RB + vtok * RB + vq * 16;
+    const uint8_t *kb = x.k + rk * RB + ktok * RB + kq * 16;
+    const uint8_t *vb = x.v + rv * RB + vtok * RB + vq * 16;
 #pragma unroll
     for (int n = 0; n < T::N16; ++n) {
       const int step = T::CH == 8 ? (n >> 1) * 4 * RB + (n & 1) * 64 : n * 4 * RB;
@@ -242,10 +245,10 @@ __device__ __forceinline__ uint32_t attn_send(const KvView &kv, int h, int t, At
       dma16(vb + n * VSTEP * RB, lds + T::VOFF + n * 1024);
     }
     if constexpr (T::SC == 256) {
-      dma4(ks + rs * SB + soff, lds + T::SOFF);
-      dma4(vs + rs * SB + soff, lds + T::SOFF + 256);
+      dma4(x.ks + rs * SB + soff, lds + T::SOFF);
+      dma4(x.vs + rs * SB + soff, lds + T::SOFF + 256);
     } else {
-      const uint8_t *q = (sside ? vs : ks) + rs * SB + soff;
+      const uint8_t *q = (sside ? x.vs : x.ks) + rs * SB + soff;
       if constexpr (SW == 16) dma16(q, lds + T::SOFF);
       else dma4(q, lds + T::SOFF);
     }
@@ -259,19 +262,6 @@ template <int D, int J, int B>
 __device__ __forceinline__ float nf4_absmax(const float *w) {
   constexpr int at = J * (D / 64) + B;
   return __builtin_bit_cast(float, row_bcast<at % 16>(__builtin_bit_cast(uint32_t, w[at / 16])));
-}
-
-// MXFP4: scale byte of position 8g + J for the lane's V values (block c /
-// (512/D)); lane c % 8 = J of the row holds the position's bytes.
-template <int D, int J>
-__device__ __forceinline__ uint32_t mx_vbyte(const uint32_t *w, int c) {
-  const int blk = c / (512 / D);
-  uint32_t x = row_bcast<J>(w[0]);
-  if constexpr (D == 256) {
-    const uint32_t y = row_bcast<J>(w[1]);                   // by every lane: the source lane must be active
-    x = blk < 4 ? x : y;
-  }
-  return (x >> ((blk & 3) * 8)) & 0xffu;
 }
 
 // The float32 that v_cvt_scalef32 takes an e8m0 byte from: it reads the
@@ -421,15 +411,9 @@ __device__ __forceinline__ void attn_tile(AttnWave<FMT, D, NQ> &w, const uint8_t
   }
   // ---- O^T += V^T P^T
   if constexpr (MX) {
-    uint32_t sb[8], vw[2] = {0, 0};
-    const int vt = g * 8 + (c & 7);
-    if constexpr (D == 64) vw[0] = *reinterpret_cast<const uint16_t *>(sc_v + vt * 2);
-    else if constexpr (D == 128) vw[0] = *reinterpret_cast<const uint32_t *>(sc_v + vt * 4);
-    else {
-      const uint2 v = *reinterpret_cast<const uint2 *>(sc_v + vt * 8);
-      vw[0] = v.x, vw[1] = v.y;
-    }
-    static_for<0, 8>([&](auto J) { sb[J] = mx_vbyte<D, J>(vw, c); });
+    uint32_t sb[8];                                          // scales of the lane's values: its block is c / (512/D)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sb[j] = sc_v[(g * 8 + j) * (D / 32) + c / (512 / D)];
     if constexpr (MASKED) {
       // A NaN scale in a place that some row does not see: 0 * NaN must not
       // reach that row. Such values are taken out of the product and their NaN
@@ -644,13 +628,19 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? (NQ == 1 && D <= 128 ? 4 : 1) : 
     // ---- S - 1 tiles under way, then the queries
     const int first = t0 + wave * 32, tiles = first < t1 ? (t1 - first + ROUND - 1) / ROUND : 0;
     uint32_t bad = 0;                                        // two bits per slot
-    AttnPages pg = attn_pages(kv, bb, first);
+    const int64_t hr = (int64_t)h << kv.page_shift;
+    AttnPlace pl;
+    pl.k = kv.k_codes + hr * (D / 2);
+    pl.v = kv.v_codes + hr * (D / 2);
+    pl.ks = static_cast<const uint8_t *>(kv.k_scales) + hr * (T::SC / 32);
+    pl.vs = static_cast<const uint8_t *>(kv.v_scales) + hr * (T::SC / 32);
+    pl.page_rows = kv.H << kv.page_shift;
+    pl.page_shift = kv.page_shift;
+    pl.n_pages = kv.n_pages;
+    attn_pages(pl, kv, bb, first + lane * ROUND);
 #pragma unroll
     for (int i = 0; i < S - 1; ++i)
-      if (i < tiles) {
-        bad |= attn_send<FMT, D>(kv, h, first + i * ROUND, pg, ring_at + i * T::BYTES, lane) << (2 * i);
-        pg = attn_pages(kv, bb, first + (i + 1) * ROUND);
-      }
+      if (i < tiles) bad |= attn_send<FMT, D>(pl, i, first + i * ROUND, ring_at + i * T::BYTES, lane) << (2 * i);
     AttnWave<FMT, D, NQ> w;
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
@@ -685,12 +675,13 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? (NQ == 1 && D <= 128 ? 4 : 1) : 
       for (int i = 0; i < KS; ++i) asm volatile("" : "+v"(w.q[n][i]));
 
     int slot = 0, next = S - 1;                              // of this tile, of the one sent now
-    for (int i = 0; i < tiles; ++i) {
-      const int t = first + i * ROUND;
-      if (i + S - 1 < tiles) {
+    // Sends the tile S - 1 further and waits for tile i.
+    auto advance = [&](int i) {
+      const int ahead = i + S - 1;
+      if (ahead < tiles) {
+        if ((ahead & 63) == 0) attn_pages(pl, kv, bb, first + (ahead + lane) * ROUND);
         bad &= ~(3u << (2 * next));
-        bad |= attn_send<FMT, D>(kv, h, t + (S - 1) * ROUND, pg, ring_at + next * T::BYTES, lane) << (2 * next);
-        pg = attn_pages(kv, bb, t + S * ROUND);
+        bad |= attn_send<FMT, D>(pl, ahead & 63, first + ahead * ROUND, ring_at + next * T::BYTES, lane) << (2 * next);
         wait_vm<(S - 1) * T::LOADS>();
       } else if (S > 3 && i + 2 < tiles) {
         wait_vm<2 * T::LOADS>();
@@ -699,14 +690,28 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? (NQ == 1 && D <= 128 ? 4 : 1) : 
       } else {
         wait_vm<0>();
       }
-      const uint32_t bd = (bad >> (2 * slot)) & 3u;
-      const uint8_t *sl = ring + slot * T::BYTES;
-      if (t >= full_lo && t + 31 <= full_hi && bd == 0)
-        attn_tile<FMT, D, NQ, false>(w, sl, false, a, lds.lut, t, lane);
-      else
-        attn_tile<FMT, D, NQ, true>(w, sl, ((bd >> (lane >> 5)) & 1u) != 0, a, lds.lut, t, lane);
+    };
+    auto done = [&] {
       slot = slot + 1 == S ? 0 : slot + 1;
       next = next + 1 == S ? 0 : next + 1;
+    };
+    auto full = [&](int i) {
+      const int t = first + i * ROUND;
+      return t >= full_lo && t + 31 <= full_hi && ((bad >> (2 * slot)) & 3u) == 0;
+    };
+    // Two loops, so that the accumulators keep their registers in each.
+    for (int i = 0; i < tiles;) {
+      for (; i < tiles && full(i); ++i) {
+        advance(i);
+        attn_tile<FMT, D, NQ, false>(w, ring + slot * T::BYTES, false, a, lds.lut, first + i * ROUND, lane);
+        done();
+      }
+      for (; i < tiles && !full(i); ++i) {
+        advance(i);
+        const bool off = ((bad >> (2 * slot + (lane >> 5))) & 1u) != 0;
+        attn_tile<FMT, D, NQ, true>(w, ring + slot * T::BYTES, off, a, lds.lut, first + i * ROUND, lane);
+        done();
+      }
     }
 
     // ---- join the waves
@@ -836,8 +841,8 @@ __global__ __launch_bounds__(kJoinThreads) void kv_attn_join_kernel(KvAttnArgs a
 template <int FMT, int D, int NQ>
 struct AttnCfg {
   static constexpr bool MX = FMT == GNF4_MXFP4;
-  static constexpr int NW = NQ == 1 && D == 64 ? 16 : D == 256 && !MX ? 4 : 8;
-  static constexpr int S = NW == 8 && MX && D == 128 ? 3 : 2;
+  static constexpr int NW = D == 256 && !MX ? 4 : 8;
+  static constexpr int S = NW == 8 && MX && D <= 128 ? 3 : 2;
 };
 
 // Rows per tile from the most new tokens of a sequence. Short contexts take a
