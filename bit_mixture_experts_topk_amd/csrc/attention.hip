@@ -699,15 +699,23 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? (NQ == 1 && D <= 128 ? 4 : 1) : 
       const int t = first + i * ROUND;
       return t >= full_lo && t + 31 <= full_hi && ((bad >> (2 * slot)) & 3u) == 0;
     };
+    // Of the waves of a SIMD the oldest is served first, and would be done a
+    // quarter of the time before the last; in turns they end together.
+    auto turn = [&](int i) {
+      if ((i ^ (wave >> 2)) & 1) __builtin_amdgcn_s_setprio(1);
+      else __builtin_amdgcn_s_setprio(0);
+    };
     // Two loops, so that the accumulators keep their registers in each.
     for (int i = 0; i < tiles;) {
       for (; i < tiles && full(i); ++i) {
         advance(i);
+        turn(i);
         attn_tile<FMT, D, NQ, false>(w, ring + slot * T::BYTES, false, a, lds.lut, first + i * ROUND, lane);
         done();
       }
       for (; i < tiles && !full(i); ++i) {
         advance(i);
+        turn(i);
         const bool off = ((bad >> (2 * slot + (lane >> 5))) & 1u) != 0;
         attn_tile<FMT, D, NQ, true>(w, ring + slot * T::BYTES, off, a, lds.lut, first + i * ROUND, lane);
         done();

@@ -53,24 +53,22 @@ hipError_t launch_kv_write(const KvRowsArgs &a, int32_t format, hipStream_t s);
 hipError_t launch_kv_read(const KvRowsArgs &a, int32_t format, int32_t out_f32, hipStream_t s);
 hipError_t launch_kv_attention(const KvAttnArgs &a, const KvAttnPlan &p, int32_t format, hipStream_t s);
 
-// The sequence that row r of the step belongs to: the last b with
-// offsets[b] <= r, or -1 when r lies before the first or behind the last
-// sequence. Called by whole waves with a uniform r. Each round the wave's
-// lanes probe 64 evenly spaced entries at once, so B <= 64 takes one load and
-// B <= 4096 two, where a bisection takes 6 and 12 in a row.
+// The last b with offsets[b] <= r, b in [0, B], or -1. Called by whole waves with
+// a uniform r. Each round the wave's lanes probe 64 evenly spaced entries at
+// once, so B < 64 takes one load and B < 4096 two, where a bisection takes 6 and
+// 12 in a row.
 __device__ __forceinline__ int find_seq(const int32_t *__restrict__ offsets, int B, int r, int lane) {
-  if (r < offsets[0] || r >= offsets[B]) return -1;
-  int lo = 0, n = B;
-  while (n > 1) {
+  int lo = 0, n = B + 1;
+  for (;;) {
     const int step = (n + 63) >> 6;
     const int i = lane * step;
     const bool below = i < n && offsets[lo + min(i, n - 1)] <= r;
     const int c = __popcll(__ballot(below));
-    if (c == 0) return -1;
+    if (c == 0) return lo - 1;
     lo += (c - 1) * step;
     n = min(step, n - (c - 1) * step);
+    if (n == 1) return lo;
   }
-  return lo;
 }
 
 // Where the row of position pos of sequence b lies: the row index in the code
@@ -81,6 +79,25 @@ __device__ __forceinline__ int64_t kv_row0(const KvView &kv, int b, int pos) {
   const int pid = kv.pages[(int64_t)b * kv.max_pages + (pos >> kv.page_shift)];
   if ((uint32_t)pid >= (uint32_t)kv.n_pages) return -1;
   return ((int64_t)pid * kv.H << kv.page_shift) + (pos & ((1 << kv.page_shift) - 1));
+}
+
+// kv_row0 of rows t0 .. t0 + n - 1 of the step (n <= 64), lane i's that of row
+// t0 + i; -1 for rows of no sequence. Called by whole waves. The sequence of t0
+// is searched for, those of the rows behind it follow from the next 64 offsets.
+__device__ __forceinline__ int64_t kv_rows(const KvView &kv, int t0, int n, int lane) {
+  const int b0 = find_seq(kv.offsets, kv.B, t0, lane);
+  const int k = b0 + 1 + lane;
+  const int next = k <= kv.B ? kv.offsets[k] : 0x7fffffff;
+  int b = b0;
+  for (int i = 1; i < n; ++i) {
+    const int c = __popcll(__ballot(next <= t0 + i));
+    // 64 offsets passed at once (empty sequences): the window does not reach
+    const int at = c < 64 ? b0 + c : find_seq(kv.offsets, kv.B, t0 + i, lane);
+    if (lane == i) b = at;
+  }
+  if (lane >= n || b < 0 || b >= kv.B) return -1;
+  const int t = t0 + lane, end = kv.offsets[b + 1];
+  return t < end && t < kv.n_tokens ? kv_row0(kv, b, kv.lens[b] - end + t) : -1;
 }
 
 }  // namespace gnf4

@@ -108,7 +108,6 @@ __device__ __forceinline__ void rotate8(float (&f)[8], const float *cs, const fl
 }
 
 // Row rr of a token: a query head, then a key head.
-template <bool BACK>
 __device__ __forceinline__ uint4 load_row(const uint16_t *q, int64_t qs, const uint16_t *k, int64_t ks, int t, int rr,
                                           int Hq, int D, int d) {
   const uint16_t *p = rr < Hq ? q + (int64_t)t * qs + (int64_t)rr * D : k + (int64_t)t * ks + (int64_t)(rr - Hq) * D;
@@ -125,8 +124,8 @@ __global__ __launch_bounds__(kRopeThreads) void norm_rope_kernel(RopeArgs a, int
   const bool in = d < a.D;
   int rr = first + sub;
   uint4 x = make_uint4(0, 0, 0, 0);
-  if (in && rr < last) x = load_row<false>(a.q, a.q_stride, a.k, a.k_stride, t, rr, a.Hq, a.D, d);
-  float wq[8], wk[8];
+  if (in && rr < last) x = load_row(a.q, a.q_stride, a.k, a.k_stride, t, rr, a.Hq, a.D, d);
+  float wq[8] = {}, wk[8] = {};
   if (a.wq && in) unpack8(*reinterpret_cast<const uint4 *>(a.wq + d), wq);
   if (a.wk && in) unpack8(*reinterpret_cast<const uint4 *>(a.wk + d), wk);
   if (a.rot) {
@@ -137,7 +136,7 @@ __global__ __launch_bounds__(kRopeThreads) void norm_rope_kernel(RopeArgs a, int
     const bool live = in && rr < last;
     const int nx = rr + RPI;
     uint4 xn = make_uint4(0, 0, 0, 0);
-    if (in && nx < last) xn = load_row<false>(a.q, a.q_stride, a.k, a.k_stride, t, nx, a.Hq, a.D, d);
+    if (in && nx < last) xn = load_row(a.q, a.q_stride, a.k, a.k_stride, t, nx, a.Hq, a.D, d);
     float f[8];
     unpack8(x, f);
     const bool isq = rr < a.Hq;
@@ -167,7 +166,7 @@ __global__ __launch_bounds__(kRopeThreads) void norm_rope_kernel(RopeArgs a, int
 // norm_rope_dw_kernel, so the result does not depend on scheduling.
 template <int LPR, bool IL>
 __global__ __launch_bounds__(kRopeThreads) void norm_rope_dx_kernel(RopeArgs a) {
-  __shared__ __attribute__((aligned(16))) float cs[128], sn[128];
+  __shared__ __attribute__((aligned(16))) float cs[2][128], sn[2][128];   // of this token and the next
   __shared__ float red[kRopeThreads * 8];
   constexpr int RPI = kRopeThreads / LPR;
   const int tid = threadIdx.x, lane = tid & 63, c = tid % LPR, sub = tid / LPR, d = 8 * c;
@@ -178,53 +177,72 @@ __global__ __launch_bounds__(kRopeThreads) void norm_rope_dx_kernel(RopeArgs a) 
   for (int i = 0; i < 8; ++i) wq[i] = wk[i] = dwq[i] = dwk[i] = 0.0f;
   if (a.wq && in) unpack8(*reinterpret_cast<const uint4 *>(a.wq + d), wq);
   if (a.wk && in) unpack8(*reinterpret_cast<const uint4 *>(a.wk + d), wk);
-  for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
-    if (a.rot) {
-      __syncthreads();
-      fill_angles(cs, sn, a, a.positions[t], tid);
-      __syncthreads();
+  // gradient and input of row rr of token t
+  auto load = [&](int t, int rr, uint4 &g, uint4 &x) {
+    g = x = make_uint4(0, 0, 0, 0);
+    if (!in || rr >= rows || t >= a.T) return;
+    g = load_row(a.dq, a.dq_stride, a.dk, a.dk_stride, t, rr, a.Hq, a.D, d);
+    if (rr < a.Hq ? a.wq != nullptr : a.wk != nullptr)
+      x = load_row(a.q, a.q_stride, a.k, a.k_stride, t, rr, a.Hq, a.D, d);
+  };
+  int t = blockIdx.x, r0 = 0, buf = 0;
+  uint4 gv, xv;
+  load(t, sub, gv, xv);
+  if (a.rot) {
+    fill_angles(cs[0], sn[0], a, a.positions[t], tid);
+    __syncthreads();
+  }
+  const float inv_d = 1.0f / (float)a.D;
+  while (t < a.T) {
+    if (r0 == 0 && a.rot && t + (int)gridDim.x < a.T)
+      fill_angles(cs[buf ^ 1], sn[buf ^ 1], a, a.positions[t + gridDim.x], tid);
+    // the next rows are under way while these are worked on
+    const int rn = r0 + RPI < rows ? r0 + RPI : 0, tn = rn ? t : t + (int)gridDim.x;
+    uint4 gn, xn;
+    load(tn, rn + sub, gn, xn);
+    const int rr = r0 + sub;
+    const bool live = in && rr < rows, isq = rr < a.Hq, norm = isq ? a.wq != nullptr : a.wk != nullptr;
+    float g[8], x[8];
+    unpack8(gv, g);
+    unpack8(xv, x);
+    if (a.rot) rotate8<IL, -1>(g, cs[buf], sn[buf], c, a.rot, lane);
+    float sq = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sq = fmaf(x[i], x[i], sq);
+    sq = row_sum<LPR>(sq);
+    const float r = 1.0f / sqrtf(sq * inv_d + a.eps);
+    float dot = 0.0f, h[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x[i] *= r;
+      h[i] = g[i] * (isq ? wq[i] : wk[i]);
+      dot = fmaf(h[i], x[i], dot);
     }
-    for (int r0 = 0; r0 < rows; r0 += RPI) {
-      const int rr = r0 + sub;
-      const bool live = in && rr < rows, isq = rr < a.Hq;
-      uint4 xv = make_uint4(0, 0, 0, 0), gv = make_uint4(0, 0, 0, 0);
-      if (live) gv = load_row<true>(a.dq, a.dq_stride, a.dk, a.dk_stride, t, rr, a.Hq, a.D, d);
-      const bool norm = isq ? a.wq != nullptr : a.wk != nullptr;
-      if (live && norm) xv = load_row<true>(a.q, a.q_stride, a.k, a.k_stride, t, rr, a.Hq, a.D, d);
-      float g[8], x[8];
-      unpack8(gv, g);
-      unpack8(xv, x);
-      if (a.rot) rotate8<IL, -1>(g, cs, sn, c, a.rot, lane);
-      float sq = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sq = fmaf(x[i], x[i], sq);
-      sq = row_sum<LPR>(sq);
-      const float r = 1.0f / sqrtf(sq / (float)a.D + a.eps);
-      float dot = 0.0f, h[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        x[i] *= r;
-        h[i] = g[i] * (isq ? wq[i] : wk[i]);
-        dot = fmaf(h[i], x[i], dot);
-      }
-      dot = row_sum<LPR>(dot) / (float)a.D;
-      if (norm) {
-        if (live) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if (isq) dwq[i] = fmaf(g[i], x[i], dwq[i]);
-            else dwk[i] = fmaf(g[i], x[i], dwk[i]);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] = r * (h[i] - x[i] * dot);
-      }
+    dot = row_sum<LPR>(dot) * inv_d;
+    if (norm) {
       if (live) {
-        uint16_t *o = isq ? a.q_out + (int64_t)t * a.q_out_stride + (int64_t)rr * a.D
-                          : a.k_out + (int64_t)t * a.k_out_stride + (int64_t)(rr - a.Hq) * a.D;
-        *reinterpret_cast<uint4 *>(o + d) = pack8(g);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (isq) dwq[i] = fmaf(g[i], x[i], dwq[i]);
+          else dwk[i] = fmaf(g[i], x[i], dwk[i]);
+        }
       }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) g[i] = r * (h[i] - x[i] * dot);
     }
+    if (live) {
+      uint16_t *o = isq ? a.q_out + (int64_t)t * a.q_out_stride + (int64_t)rr * a.D
+                        : a.k_out + (int64_t)t * a.k_out_stride + (int64_t)(rr - a.Hq) * a.D;
+      *reinterpret_cast<uint4 *>(o + d) = pack8(g);
+    }
+    if (rn == 0 && a.rot) {
+      __syncthreads();                                       // the next token's angles are there
+      buf ^= 1;
+    }
+    gv = gn;
+    xv = xn;
+    r0 = rn;
+    t = tn;
   }
   if (!a.part) return;
 #pragma unroll
@@ -241,25 +259,33 @@ __global__ __launch_bounds__(kRopeThreads) void norm_rope_dx_kernel(RopeArgs a) 
   }
 }
 
-// Sums the workgroups' parts: 16 columns of the 2 D per workgroup, 16 slices of
+// Sums the workgroups' parts: 16 columns of the 2 D per workgroup, 64 slices of
 // the parts each, joined in LDS.
-__global__ __launch_bounds__(256) void norm_rope_dw_kernel(const float *__restrict__ part, int n, int D,
-                                                            float *__restrict__ dwq, float *__restrict__ dwk) {
-  __shared__ float red[16][17];
+constexpr int kDwSlices = 64;
+
+__global__ __launch_bounds__(16 * kDwSlices) void norm_rope_dw_kernel(const float *__restrict__ part, int n, int D,
+                                                                      float *__restrict__ dwq,
+                                                                      float *__restrict__ dwk) {
+  __shared__ float red[kDwSlices][17];
   const int col = threadIdx.x & 15, slice = threadIdx.x >> 4, j = (int)blockIdx.x * 16 + col;
   float s = 0.0f;
   if (j < 2 * D) {
 #pragma unroll 8
-    for (int i = slice; i < n; i += 16) s += part[(int64_t)i * 2 * D + j];
+    for (int i = slice; i < n; i += kDwSlices) s += part[(int64_t)i * 2 * D + j];
   }
   red[slice][col] = s;
   __syncthreads();
-  if (slice == 0 && j < 2 * D) {
+  if (threadIdx.x < 64) {                                    // four lanes per column
+    const int q = threadIdx.x >> 4;
     float v = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v += red[i][col];
-    float *o = j < D ? dwq : dwk;
-    if (o) o[j < D ? j : j - D] = v;
+    for (int i = 0; i < kDwSlices / 4; ++i) v += red[q * (kDwSlices / 4) + i][col];
+    v += __shfl_xor(v, 16, 64);
+    v += __shfl_xor(v, 32, 64);
+    if (q == 0 && j < 2 * D) {
+      float *o = j < D ? dwq : dwk;
+      if (o) o[j < D ? j : j - D] = v;
+    }
   }
 }
 
@@ -303,7 +329,7 @@ hipError_t launch_norm_rope_dx(const RopeArgs &a, hipStream_t s) {
     if (e != hipSuccess) return e;
   }
   if (!a.dwq && !a.dwk) return hipSuccess;
-  hipLaunchKernelGGL(norm_rope_dw_kernel, dim3((2 * a.D + 15) / 16), dim3(256), 0, s, a.part, n, a.D, a.dwq, a.dwk);
+  hipLaunchKernelGGL(norm_rope_dw_kernel, dim3((2 * a.D + 15) / 16), dim3(16 * kDwSlices), 0, s, a.part, n, a.D, a.dwq, a.dwk);
   return hipGetLastError();
 }
 

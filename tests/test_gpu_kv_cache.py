@@ -121,6 +121,26 @@ def test_midpoints_and_neighbours(fmt):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+def test_every_quotient_of_two_significands(fmt):
+    """A block's largest value with each of the 128 bf16 significands, against
+    every significand at ten binades, of both signs."""
+    say("kv write, all quotients", fmt)
+    top = 0x3f80 + np.arange(128)                            # [1, 2)
+    rows = []
+    for e in range(10):
+        w = 0x3f80 + np.arange(128) - 128 * e
+        for a in top:
+            for part in w.reshape(2, 64):
+                ok = np.where(part <= a, part, a)            # not above the largest
+                rows.append(np.concatenate((ok[:63], [a])))
+                rows.append(np.concatenate(([a], ok[1:] | 0x8000)))
+    x = np.array(rows, dtype=np.uint16).reshape(-1, 4, 64)
+    T = x.shape[0]
+    f = oa.bf16_to_f64(x)
+    run_write(fmt, Step([T], [T], 64), 4, 64, f, -f, dev_bf16(x), dev_bf16(x ^ 0x8000))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 def test_nan_and_infinity_mark_their_block(fmt):
     g = gnf4()
     say("kv write NaN / inf", fmt)
