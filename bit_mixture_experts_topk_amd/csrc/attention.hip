@@ -92,17 +92,28 @@ constexpr int kAttnUnit = 128;
 // Arrays that no kernel writes meanwhile: scalar loads where the index is uniform.
 typedef const __attribute__((address_space(4))) int32_t *const_ints;
 
-__device__ __forceinline__ AttnSeq attn_seq(const KvAttnArgs &a, int b, int M) {
-  const KvView &kv = a.kv;
-  AttnSeq x;
+// What the arrays say of sequence b: first row, rows, length.
+struct AttnRaw {
+  int r0, n, len;
+};
+
+__device__ __forceinline__ AttnRaw attn_raw(const KvView &kv, int b) {
   const const_ints off = (const_ints)(uintptr_t)kv.offsets, lens = (const_ints)(uintptr_t)kv.lens;
-  const int o0 = off[b], o1 = off[b + 1], len = lens[b];
+  const int o0 = off[b], o1 = off[b + 1];
   const int e = min(max(o1, 0), kv.n_tokens);
+  AttnRaw x;
   x.r0 = min(max(o0, 0), e);
-  const int n = e - x.r0;
-  x.rows = n * a.G;
-  x.start = len - n;
-  x.hi = (int)min((int64_t)len, (int64_t)kv.max_pages << kv.page_shift);
+  x.n = e - x.r0;
+  x.len = lens[b];
+  return x;
+}
+
+__device__ __forceinline__ AttnSeq attn_seq(const KvAttnArgs &a, const AttnRaw &s, int M) {
+  AttnSeq x;
+  x.r0 = s.r0;
+  x.rows = s.n * a.G;
+  x.start = s.len - s.n;
+  x.hi = (int)min((int64_t)s.len, (int64_t)a.kv.max_pages << a.kv.page_shift);
   x.lo = a.window > 0 ? max(0, x.start - a.window + 1) & ~31 : 0;
   x.mts = min((x.rows + M - 1) / M, a.n_mt);
   x.units = x.hi > x.lo ? (x.hi - x.lo + kAttnUnit - 1) / kAttnUnit : 1;
@@ -123,11 +134,27 @@ __device__ __forceinline__ int wave_scan(int v) {
 
 __device__ __forceinline__ int attn_units(const KvAttnArgs &a, const AttnSeq &x) { return x.mts * a.kv.H * x.units; }
 
-// Running sum of the units of the 64 sequences from b0 on, one per lane.
-__device__ __forceinline__ int attn_sums(const KvAttnArgs &a, int b0, int M, int lane) {
+// 64 sequences from b0 on, one per lane, and the running sum of their units.
+struct AttnChunk {
+  AttnRaw s;
+  int sum;
+};
+
+__device__ __forceinline__ AttnChunk attn_chunk(const KvAttnArgs &a, int b0, int M, int lane) {
   const int b = b0 + lane;
-  const AttnSeq x = attn_seq(a, min(b, a.kv.B - 1), M);
-  return wave_scan(b < a.kv.B ? attn_units(a, x) : 0);
+  AttnChunk k;
+  k.s = attn_raw(a.kv, min(b, a.kv.B - 1));
+  if (b >= a.kv.B) k.s.n = 0;
+  k.sum = wave_scan(attn_units(a, attn_seq(a, k.s, M)));
+  return k;
+}
+
+__device__ __forceinline__ AttnRaw attn_pick(const AttnChunk &k, int l) {
+  AttnRaw s;
+  s.r0 = __builtin_amdgcn_readlane(k.s.r0, l);
+  s.n = __builtin_amdgcn_readlane(k.s.n, l);
+  s.len = __builtin_amdgcn_readlane(k.s.len, l);
+  return s;
 }
 
 // Lane N of the lane's row of 16.
@@ -572,22 +599,20 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? (NQ == 1 && D <= 128 ? 4 : 1) : 
   const uint8_t *ring = lds.ring + wave * S * T::BYTES;
   const uint32_t ring_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)ring;
   const int Hq = kv.H * a.G;
-  if constexpr (!MX) {
-    fill_nf4_lut<NT>(lds.lut, tid);
-    __syncthreads();
-  }
+  if constexpr (!MX) fill_nf4_lut<NT>(lds.lut, tid);         // read after the barrier below
 
   // ---- the share [u, end) of the runs, by every wave for itself
   int u = 0, end = 0, b0 = 0, base = 0;                      // base: runs before sequence b0
-  int sum = 0;
+  AttnChunk k;
   if (a.shared) {
-    sum = attn_sums(a, 0, M, lane);
-    int total = __builtin_amdgcn_readlane(sum, 63);
-    for (int i = 64; i < kv.B; i += 64) total += __builtin_amdgcn_readlane(attn_sums(a, i, M, lane), 63);
+    k = attn_chunk(a, 0, M, lane);
+    int total = __builtin_amdgcn_readlane(k.sum, 63);
+    for (int i = 64; i < kv.B; i += 64) total += __builtin_amdgcn_readlane(attn_chunk(a, i, M, lane).sum, 63);
     const int share = attn_share(total);
     u = blockIdx.x * share;
     end = min(total, u + share);
   }
+  if constexpr (!MX) __syncthreads();
 
   for (;;) {
     // ---- the next problem: tile mt, head h of sequence bb; its runs [q0, q1)
@@ -596,15 +621,15 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? (NQ == 1 && D <= 128 ? 4 : 1) : 
     if (a.shared) {
       if (u >= end) return;
       uint64_t past;
-      while ((past = __ballot(base + sum > u)) == 0) {       // sequences without rows have no runs
-        base += __builtin_amdgcn_readlane(sum, 63);
+      while ((past = __ballot(base + k.sum > u)) == 0) {     // sequences without rows have no runs
+        base += __builtin_amdgcn_readlane(k.sum, 63);
         b0 += 64;
-        sum = attn_sums(a, b0, M, lane);
+        k = attn_chunk(a, b0, M, lane);
       }
       const int l = __builtin_ctzll(past);
       bb = b0 + l;
-      x = attn_seq(a, bb, M);
-      const int rel = u - (base + __builtin_amdgcn_readlane(sum, l) - attn_units(a, x));
+      x = attn_seq(a, attn_pick(k, l), M);
+      const int rel = u - (base + __builtin_amdgcn_readlane(k.sum, l) - attn_units(a, x));
       const int item = rel / x.units;
       q0 = rel - item * x.units;
       mt = item / kv.H;
@@ -617,7 +642,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? (NQ == 1 && D <= 128 ? 4 : 1) : 
       idx /= kv.H;
       mt = idx % a.n_mt;
       bb = idx / a.n_mt;
-      x = attn_seq(a, bb, M);
+      x = attn_seq(a, attn_raw(kv, bb), M);
       if (mt >= x.mts) return;
       q1 = x.units;
     }
@@ -743,13 +768,14 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? (NQ == 1 && D <= 128 ? 4 : 1) : 
       for (int v = 1; v < NW; ++v) top = fmaxf(top, lds.sm[v][r]);
       const float f = __builtin_amdgcn_exp2f(w.m[n] - (top == kNegInf ? 0.0f : top));
       float *mine = lds.red + (wave * 16 + c) * (D + 4);
+      // four values of the row at a time: MXFP4 row index 4g + i of every tile d
+      // is value (4g + i) D/16 + d, NF4 value 64 (d / 4) + 4 (4g + i) + d % 4
 #pragma unroll
-      for (int d = 0; d < ND; ++d)
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int cc = g * 4 + i;
-          mine[MX ? cc * (D / 16) + d : (d >> 2) * 64 + cc * 4 + (d & 3)] = w.o[n][d][i] * f;
-        }
+        for (int d = 0; d < ND; d += 4)
+          *reinterpret_cast<float4 *>(mine + (MX ? (g * 4 + i) * (D / 16) + d : d * 16 + (g * 4 + i) * 4)) =
+              make_float4(w.o[n][d][i] * f, w.o[n][d + 1][i] * f, w.o[n][d + 2][i] * f, w.o[n][d + 3][i] * f);
       __syncthreads();
       for (int k4 = tid; k4 < 16 * (D / 4); k4 += NT) {
         const int rr = k4 / (D / 4), d4 = (k4 - rr * (D / 4)) * 4;
@@ -800,10 +826,10 @@ __global__ __launch_bounds__(kJoinThreads) void kv_attn_join_kernel(KvAttnArgs a
   const int h = idx % kv.H;
   idx /= kv.H;
   const int mt = idx % a.n_mt, b = idx / a.n_mt;
-  const AttnSeq x = attn_seq(a, b, M);
+  const AttnSeq x = attn_seq(a, attn_raw(kv, b), M);
   int first = 0, total = 0;
   for (int i = 0; i < kv.B; i += 64) {
-    const int sum = attn_sums(a, i, M, lane);
+    const int sum = attn_chunk(a, i, M, lane).sum;
     if (b >= i && b < i + 64) first = total + __builtin_amdgcn_readlane(sum, b - i) - attn_units(a, x);
     total += __builtin_amdgcn_readlane(sum, 63);
   }
