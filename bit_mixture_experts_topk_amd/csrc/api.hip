@@ -872,7 +872,7 @@ static gnf4_status attention_plan(const gnf4_kv_cache *c, const gnf4_kv_batch *b
   const int64_t capacity = (int64_t)b->max_pages * c->page_size;
   const int64_t len = std::min<int64_t>(std::max(b->max_len, 1), capacity);
   if ((int64_t)b->n_tokens * (Hq / c->H) > 0x3fffffffLL ||
-      !kv_attention_plan(c->D, c->H, Hq / c->H, b->B, b->n_tokens, most, len, capacity, window, p))
+      !kv_attention_plan(c->format, c->D, c->H, Hq / c->H, b->B, b->n_tokens, most, len, capacity, window, p))
     return fail(GNF4_ERR_UNSUPPORTED, "too many rows for one call");
   return ok();
 }

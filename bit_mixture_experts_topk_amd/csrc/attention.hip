@@ -82,9 +82,9 @@ __device__ __forceinline__ bf16x8_t op8(uint32_t a, uint32_t b, uint32_t c, uint
 struct AttnSeq {
   int r0, rows;                   // first token row, query rows (tokens * G)
   int start;                      // position of its first new token
-  int lo, hi;                     // positions that any row may see, lo a multiple of 32
-  int mts, units;                 // row tiles; runs of 128 positions per tile and head (at least one: it
-                                  // writes the result)
+  int hi;                         // end of the positions that any row may see
+  int mts, units;                 // row tiles; runs of 128 positions per tile and head, from the first
+                                  // that the tile sees on (at least one: it writes the result)
 };
 
 constexpr int kAttnUnit = 128;
@@ -114,9 +114,10 @@ __device__ __forceinline__ AttnSeq attn_seq(const KvAttnArgs &a, const AttnRaw &
   x.rows = s.n * a.G;
   x.start = s.len - s.n;
   x.hi = (int)min((int64_t)s.len, (int64_t)a.kv.max_pages << a.kv.page_shift);
-  x.lo = a.window > 0 ? max(0, x.start - a.window + 1) & ~31 : 0;
   x.mts = min((x.rows + M - 1) / M, a.n_mt);
-  x.units = x.hi > x.lo ? (x.hi - x.lo + kAttnUnit - 1) / kAttnUnit : 1;
+  int span = x.hi;
+  if (a.window > 0) span = (int)min((int64_t)span, (int64_t)a.window + a.tile_tokens - 1 + 31);
+  x.units = span > 0 ? (span + kAttnUnit - 1) / kAttnUnit : 1;
   return x;
 }
 
@@ -307,21 +308,40 @@ __device__ __forceinline__ void static_for(F &&f) {
 template <int FMT, int D, int NQ>
 struct AttnWave {
   static constexpr int KS = D / 32, ND = D / 16;
-  bf16x8_t q[NQ][KS];
+  static constexpr bool QLDS = NQ > 2;                       // more tiles: their queries stay in LDS
+  bf16x8_t q[QLDS ? 1 : NQ][QLDS ? 1 : KS];
   f32x4_t o[NQ][ND];
   float m[NQ], l[NQ];
   int qpos[NQ];                                              // position of the lane's query row
 };
 
+// The NF4 byte table of common.h with 64 >> LS copies: entry b of copy c at byte
+// (b * 64 + c) * 4 >> LS. With fewer copies a lane's address takes one more
+// instruction, and lanes of one copy meet in a bank.
+template <int LS>
+__device__ __forceinline__ uint32_t attn_lut(const uint32_t *lut, uint32_t w, uint32_t lane4, int byte) {
+  return lut_read(lut, lut_addr(w, lane4, byte) >> LS);
+}
+
+template <int LS, int NT>
+__device__ __forceinline__ void fill_attn_lut(uint32_t *lut, int tid) {
+#pragma unroll
+  for (int i = 0; i < (4096 >> LS) / NT; ++i) {
+    const uint32_t grp = (uint32_t)tid + NT * i, b = grp >> (4 - LS);
+    const uint32_t v = nf4_bf16(b >> 4) | (nf4_bf16(b & 15u) << 16);
+    *reinterpret_cast<uint4 *>(lut + grp * 4) = make_uint4(v, v, v, v);
+  }
+}
+
 // One tile from its slot sl. bad: the lane's positions 8g..8g+7 lie on no page.
-template <int FMT, int D, int NQ, bool MASKED>
+template <int FMT, int D, int NQ, bool MASKED, int LS>
 __device__ __forceinline__ void attn_tile(AttnWave<FMT, D, NQ> &w, const uint8_t *sl, bool bad, const KvAttnArgs &a,
-                                          const uint32_t *lut, int t, int lane) {
+                                          const uint32_t *lut, const uint4 *ql, int t, int lane) {
   typedef AttnSlot<FMT, D> T;
   constexpr bool MX = FMT == GNF4_MXFP4;
   constexpr int KS = D / 32, ND = D / 16;
   const int c = lane & 15, g = lane >> 4;
-  const uint32_t lane4 = (uint32_t)lane * 4;
+  const uint32_t lane4 = (uint32_t)(lane & ((64 >> LS) - 1)) << (2 + LS);
   float s[NQ][8];
   const uint8_t *sc_k = sl + T::SOFF, *sc_v = sc_k + T::SC;
   float ksn[2], vsn[2];                                      // NF4: absmax over the operand codebook's scale
@@ -368,16 +388,19 @@ __device__ __forceinline__ void attn_tile(AttnWave<FMT, D, NQ> &w, const uint8_t
         const float sc = e8m0_scale(D == 256 ? (k < KS / 2 ? kb & 0xffu : kb >> 8) : kb);
         ka = op8(fp4_pair<0>(kw, sc), fp4_pair<1>(kw, sc), fp4_pair<2>(kw, sc), fp4_pair<3>(kw, sc));
       } else {
-        ka = op8(lut_read(lut, lut_addr(kw, lane4, 0)), lut_read(lut, lut_addr(kw, lane4, 1)),
-                 lut_read(lut, lut_addr(kw, lane4, 2)), lut_read(lut, lut_addr(kw, lane4, 3)));
+        ka = op8(attn_lut<LS>(lut, kw, lane4, 0), attn_lut<LS>(lut, kw, lane4, 1),
+                 attn_lut<LS>(lut, kw, lane4, 2), attn_lut<LS>(lut, kw, lane4, 3));
       }
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
         constexpr f32x4_t zero = {0, 0, 0, 0};
+        bf16x8_t qv;
+        if constexpr (AttnWave<FMT, D, NQ>::QLDS) qv = __builtin_bit_cast(bf16x8_t, ql[(n * KS + k) * 64 + lane]);
+        else qv = w.q[n][k];
         if constexpr (MX)
-          acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ka, w.q[n][k], k == 0 ? zero : acc[n], 0, 0, 0);
+          acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ka, qv, k == 0 ? zero : acc[n], 0, 0, 0);
         else
-          blk[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ka, w.q[n][k], (k & 1) == 0 ? zero : blk[n], 0, 0, 0);
+          blk[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ka, qv, (k & 1) == 0 ? zero : blk[n], 0, 0, 0);
       }
       if constexpr (!MX && (k & 1)) {                        // a block of 64 is complete
         static_for<0, 4>([&](auto J) {
@@ -531,7 +554,7 @@ __device__ __forceinline__ void attn_tile(AttnWave<FMT, D, NQ> &w, const uint8_t
       for (int y = 0; y < 2; ++y) {
         uint32_t pr[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) pr[j] = lut_read(lut, lut_addr(vc[j], lane4, y));
+        for (int j = 0; j < 8; ++j) pr[j] = attn_lut<LS>(lut, vc[j], lane4, y);
         uint32_t e[4], f[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -577,20 +600,23 @@ __device__ __forceinline__ AttnScale attn_finish(float m, float l, const float *
 __device__ __forceinline__ int attn_share(int total) { return (total + kAttnGroups - 1) / kAttnGroups; }
 
 template <int FMT, int D, int NQ, int NW, int S>
-__global__ __launch_bounds__(64 * NW, NW == 4 ? (NQ == 1 && D <= 128 ? 4 : 1) : NW / 4) void kv_attn_kernel(KvAttnArgs a) {
+__global__ __launch_bounds__(64 * NW, NW == 4 ? (D == 256 ? 1 : NQ == 1 ? 3 : 2) : NW / 4) void kv_attn_kernel(KvAttnArgs a) {
   typedef AttnSlot<FMT, D> T;
   constexpr bool MX = FMT == GNF4_MXFP4;
   constexpr int NT = 64 * NW, ROUND = 32 * NW;
   constexpr int KS = D / 32, ND = D / 16, M = 16 * NQ;
+  constexpr bool QLDS = AttnWave<FMT, D, NQ>::QLDS;
+  constexpr int LS = NW == 4 && D <= 128 ? 2 : 0;
   // one block, so that the table starts at LDS address 0 and a byte's address
   // is what lut_addr forms
   struct Lds {
-    uint32_t lut[MX ? 4 : kLutWords];
+    uint32_t lut[MX ? 4 : kLutWords >> LS];
     union {
       uint8_t ring[NW * S * T::BYTES];                       // S slots of every wave
       float red[NW * 16 * (D + 4)];                          // the waves' O tile, when they join
     };
     float sm[NW][M], sl[NW][M];
+    uint4 q[QLDS ? NQ * KS * 64 : 1];                        // lane's operand of (tile n, step k) at (n KS + k) 64 + lane
   };
   __shared__ __attribute__((aligned(16))) Lds lds;
   const KvView &kv = a.kv;
@@ -599,7 +625,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? (NQ == 1 && D <= 128 ? 4 : 1) : 
   const uint8_t *ring = lds.ring + wave * S * T::BYTES;
   const uint32_t ring_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)ring;
   const int Hq = kv.H * a.G;
-  if constexpr (!MX) fill_nf4_lut<NT>(lds.lut, tid);         // read after the barrier below
+  if constexpr (!MX) fill_attn_lut<LS, NT>(lds.lut, tid);         // read after the barrier below
 
   // ---- the share [u, end) of the runs, by every wave for itself
   int u = 0, end = 0, b0 = 0, base = 0;                      // base: runs before sequence b0
@@ -647,8 +673,16 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? (NQ == 1 && D <= 128 ? 4 : 1) : 
       q1 = x.units;
     }
     const bool whole = q0 == 0 && q1 == x.units;
-    const int t0 = x.lo + q0 * kAttnUnit, row0 = mt * M;
-    const int t1 = q1 == x.units ? x.hi : x.lo + q1 * kAttnUnit;
+    // Tiles of late tokens see more than those of early ones: they alternate, so
+    // that shares of several tiles come out alike.
+    mt = (mt & 1) ? x.mts - 1 - (mt >> 1) : mt >> 1;
+    const int row0 = mt * M, last = min(row0 + M, x.rows) - 1;
+    const int full_hi = x.start + row0 / a.G;                // every row sees from full_lo to full_hi
+    const int full_lo = a.window > 0 ? x.start + last / a.G - a.window + 1 : 0;
+    // the run's positions, among those that some row of this tile sees
+    const int lo = a.window > 0 ? max(0, full_hi - a.window + 1) & ~31 : 0;
+    const int hi = min(x.hi, x.start + last / a.G + 1);
+    const int t0 = lo + q0 * kAttnUnit, t1 = q1 == x.units ? hi : min(hi, lo + q1 * kAttnUnit);
 
     // ---- S - 1 tiles under way, then the queries
     const int first = t0 + wave * 32, tiles = first < t1 ? (t1 - first + ROUND - 1) / ROUND : 0;
@@ -678,26 +712,29 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? (NQ == 1 && D <= 128 ? 4 : 1) : 
 #pragma unroll
       for (int i = 0; i < KS; ++i) {
         const int d = MX ? g * (D / 4) + i * 8 : (i >> 1) * 64 + g * 16 + (i & 1) * 8;
+        if (QLDS && (n * KS + i) % NW != wave) continue;     // the waves share the loading
         uint4 v = make_uint4(0, 0, 0, 0);
         if (ok) v = *reinterpret_cast<const uint4 *>(qp + d);
         v.x ^= a.q_sign;
         v.y ^= a.q_sign;
         v.z ^= a.q_sign;
         v.w ^= a.q_sign;
-        w.q[n][i] = __builtin_bit_cast(bf16x8_t, v);
+        if constexpr (QLDS) lds.q[(n * KS + i) * 64 + lane] = v;
+        else w.q[n][i] = __builtin_bit_cast(bf16x8_t, v);
       }
 #pragma unroll
       for (int d = 0; d < ND; ++d) w.o[n][d] = f32x4_t{0, 0, 0, 0};
     }
-    const int last = min(row0 + M, x.rows) - 1;
-    const int full_hi = x.start + row0 / a.G;                // every row sees from full_lo to full_hi
-    const int full_lo = a.window > 0 ? x.start + last / a.G - a.window + 1 : 0;
     // The queries are here before the loop: a wait for them inside it would be
     // one for the tiles under way as well.
+    if constexpr (QLDS) {
+      __syncthreads();
+    } else {
 #pragma unroll
-    for (int n = 0; n < NQ; ++n)
+      for (int n = 0; n < NQ; ++n)
 #pragma unroll
-      for (int i = 0; i < KS; ++i) asm volatile("" : "+v"(w.q[n][i]));
+        for (int i = 0; i < KS; ++i) asm volatile("" : "+v"(w.q[n][i]));
+    }
 
     int slot = 0, next = S - 1;                              // of this tile, of the one sent now
     // Sends the tile S - 1 further and waits for tile i.
@@ -735,14 +772,14 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? (NQ == 1 && D <= 128 ? 4 : 1) : 
       for (; i < tiles && full(i); ++i) {
         advance(i);
         turn(i);
-        attn_tile<FMT, D, NQ, false>(w, ring + slot * T::BYTES, false, a, lds.lut, first + i * ROUND, lane);
+        attn_tile<FMT, D, NQ, false, LS>(w, ring + slot * T::BYTES, false, a, lds.lut, lds.q, first + i * ROUND, lane);
         done();
       }
       for (; i < tiles && !full(i); ++i) {
         advance(i);
         turn(i);
         const bool off = ((bad >> (2 * slot + (lane >> 5))) & 1u) != 0;
-        attn_tile<FMT, D, NQ, true>(w, ring + slot * T::BYTES, off, a, lds.lut, first + i * ROUND, lane);
+        attn_tile<FMT, D, NQ, true, LS>(w, ring + slot * T::BYTES, off, a, lds.lut, lds.q, first + i * ROUND, lane);
         done();
       }
     }
@@ -825,7 +862,8 @@ __global__ __launch_bounds__(kJoinThreads) void kv_attn_join_kernel(KvAttnArgs a
   int idx = (int)blockIdx.x;
   const int h = idx % kv.H;
   idx /= kv.H;
-  const int mt = idx % a.n_mt, b = idx / a.n_mt;
+  int mt = idx % a.n_mt;
+  const int b = idx / a.n_mt;
   const AttnSeq x = attn_seq(a, attn_raw(kv, b), M);
   int first = 0, total = 0;
   for (int i = 0; i < kv.B; i += 64) {
@@ -839,6 +877,7 @@ __global__ __launch_bounds__(kJoinThreads) void kv_attn_join_kernel(KvAttnArgs a
   const int w0 = first / share, w1 = (first + x.units - 1) / share;
   if (w0 == w1) return;                                      // written by its only workgroup
   const int n = w1 - w0 + 1;
+  mt = (mt & 1) ? x.mts - 1 - (mt >> 1) : mt >> 1;           // the order of the shares
   const float2 *ml = reinterpret_cast<const float2 *>(a.part + 2LL * kAttnGroups * M * D);
   for (int u = tid; u < M * (D / 4); u += kJoinThreads) {
     const int r = u / (D / 4), d4 = (u - r * (D / 4)) * 4, row = mt * M + r;
@@ -879,21 +918,33 @@ struct AttnCfg {
   static constexpr int S = NW == 8 && MX && D <= 128 ? 3 : 2;
 };
 
+// The most 16-row tiles of a wave whose results the registers hold: a step
+// decodes K and V once for all of them.
+constexpr int attn_most_tiles(int format, int D) {
+  return D == 256 ? 1 : D == 64 ? 4 : format == GNF4_MXFP4 ? 3 : 2;
+}
+
+constexpr int kAttnShort = 1024;
+
 // Rows per tile from the most new tokens of a sequence. Short contexts take a
 // workgroup per problem and one launch; where these are at least as many as
 // compute units, of four waves, so that several fit on one.
-bool kv_attention_plan(int32_t D, int32_t H, int32_t G, int32_t B, int64_t n_tokens, int32_t max_new,
+bool kv_attention_plan(int32_t format, int32_t D, int32_t H, int32_t G, int32_t B, int64_t n_tokens, int32_t max_new,
                        int64_t max_len, int64_t capacity, int32_t window, KvAttnPlan *p) {
   const int64_t rows = (int64_t)max_new * G;
-  p->nq = rows <= 16 || D == 256 ? 1 : 2;                     // D = 256: the registers hold no second tile
+  p->nq = rows <= 16 || D == 256 ? 1 : rows <= 32 ? 2 : attn_most_tiles(format, D);
+  // a short context is a small problem also with many rows
+  const int64_t seen = window > 0 ? std::min<int64_t>(max_len, (int64_t)window + 64) : max_len;
+  if (seen <= kAttnShort && p->nq > 2) p->nq = 2;
   const int M = 16 * p->nq;
   const int64_t n_mt = (rows + M - 1) / M;
   p->items = (int64_t)B * n_mt * H;
   int64_t len = std::max<int64_t>(max_len, 1);
-  if (window > 0) len = std::min<int64_t>(len, (int64_t)window + max_new - 1 + 31);
+  p->tile_tokens = (int32_t)std::min<int64_t>((M - 1 + G - 1) / G + 1, max_new);
+  if (window > 0) len = std::min<int64_t>(len, (int64_t)window + p->tile_tokens - 1 + 31);
   if (p->items > 0x7fffffffLL) return false;
   p->n_mt = (int32_t)n_mt;
-  p->shared = len > 1024;
+  p->shared = len > kAttnShort;
   p->small = !p->shared && p->items >= kAttnGroups;
   // the runs are counted in 32 bits
   if (p->shared && p->items * ((capacity + kAttnUnit - 1) / kAttnUnit) > 0x7fffffffLL) p->shared = 0;
@@ -914,6 +965,9 @@ static hipError_t attn_go(const KvAttnArgs &a, const KvAttnPlan &p, hipStream_t 
 template <int FMT, int D>
 static hipError_t attn_nq(const KvAttnArgs &a, const KvAttnPlan &p, hipStream_t s) {
   if constexpr (D <= 128) {
+    if (p.small && p.nq == 2) return attn_go<FMT, D, 2, 4, 2>(a, p, s);
+    constexpr int most = attn_most_tiles(FMT, D);
+    if (p.nq == most && most > 2) return attn_go<FMT, D, most, AttnCfg<FMT, D, most>::NW, AttnCfg<FMT, D, most>::S>(a, p, s);
     if (p.nq == 2) return attn_go<FMT, D, 2, AttnCfg<FMT, D, 2>::NW, AttnCfg<FMT, D, 2>::S>(a, p, s);
   }
   if (p.small) return attn_go<FMT, D, 1, 4, 2>(a, p, s);
@@ -924,6 +978,7 @@ hipError_t launch_kv_attention(const KvAttnArgs &args, const KvAttnPlan &p, int3
   KvAttnArgs a = args;
   a.n_mt = p.n_mt;
   a.shared = p.shared;
+  a.tile_tokens = p.tile_tokens;
   // The running maximum is taken before the scale, which therefore must not be
   // negative (the queries change sign instead) nor 0 (0 times the -inf of a
   // masked place; 2^-100 leaves the weights equal).

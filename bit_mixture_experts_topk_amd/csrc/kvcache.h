@@ -36,18 +36,19 @@ struct KvAttnArgs {
   float scale_log2;               // scale * log2(e): the softmax runs in base 2
   uint32_t q_sign;                // flips the queries' signs (a negative scale)
   int32_t n_mt;                   // most row tiles of one sequence
+  int32_t tile_tokens;            // most tokens that the rows of one tile belong to
   int32_t shared;                 // 1: equal shares of all work per workgroup; 0: a workgroup per tile
   float *part;                    // [slots][M][D] then [slots][M][2], two slots per workgroup
 };
 
 // How one call is cut (attention.hip).
 struct KvAttnPlan {
-  int32_t nq, n_mt, shared, small;
+  int32_t nq, n_mt, shared, small, tile_tokens;
   int64_t items;                  // sequences * n_mt * H
   size_t bytes;
 };
-bool kv_attention_plan(int32_t D, int32_t H, int32_t G, int32_t B, int64_t n_tokens, int32_t max_new,
-                       int64_t max_len, int64_t capacity, int32_t window, KvAttnPlan *p);
+bool kv_attention_plan(int32_t format, int32_t D, int32_t H, int32_t G, int32_t B, int64_t n_tokens,
+                       int32_t max_new, int64_t max_len, int64_t capacity, int32_t window, KvAttnPlan *p);
 
 hipError_t launch_kv_write(const KvRowsArgs &a, int32_t format, hipStream_t s);
 hipError_t launch_kv_read(const KvRowsArgs &a, int32_t format, int32_t out_f32, hipStream_t s);
