@@ -25,7 +25,7 @@
 // compute unit has about 70 KB under way and its registers hold four waves per
 // SIMD, which cover each other's latencies.
 //
-// No transposes. v_mfma_f32_16x16x32_bf16 takes A rows from lanes 0..15 with 8
+// No transposes. v_mfma_f32_16x16x32 (bf16 or f16) takes A rows from lanes 0..15 with 8
 // consecutive k per lane group g = lane / 16, and leaves C with its column in
 // the lane and rows 4g..4g+3 in the registers. Computed are S^T = K Q^T (rows =
 // positions, columns = query rows) and O^T = V^T P^T. Row r of K tile i (of
@@ -72,6 +72,49 @@ __device__ __forceinline__ uint32_t pk_bf16(float a, float b) {
   typedef float f32x2_t __attribute__((ext_vector_type(2)));
   const f32x2_t v = {a, b};
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_t));
+}
+
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ uint32_t pk_f16(float a, float b) {
+  typedef float f32x2_t __attribute__((ext_vector_type(2)));
+  typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+  const f32x2_t v = {a, b};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2_t));
+}
+
+// The product type of a format: bf16 holds MXFP4 values exactly at every scale.
+// NF4 takes fp16, whose three more bits matter there: a codebook value's
+// rounding is the same wherever the code occurs, so it does not average out
+// over positions as the values themselves do (bf16 left 6e-3 of a result over
+// 4500 positions). Its operands are kept in fp16's range: codes are at most
+// s, queries and probabilities are brought there by powers of two.
+template <int FMT>
+__device__ __forceinline__ f32x4_t mfma_16x16x32(bf16x8_t a, bf16x8_t b, f32x4_t c) {
+  if constexpr (FMT == GNF4_MXFP4)
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0,
+                                                  0, 0);
+}
+
+// The float32 s in [1, 2) with the least mean of (fp16(s c[q]) / s - c[q])^2 over
+// the 16 codes (2.5x below s = 1 in the root); results are scaled by 1/s.
+constexpr float kNF4HalfScale = 1.6776896715164185f;
+constexpr float kNF4HalfInv = 1.0f / kNF4HalfScale;
+
+constexpr uint64_t nf4_f16_bits(int q) {
+  return __builtin_bit_cast(uint16_t, (_Float16)(__builtin_bit_cast(float, kNF4Bits[q & 15]) * kNF4HalfScale));
+}
+
+__device__ __forceinline__ uint32_t nf4_f16(uint32_t q) {
+  constexpr uint64_t w[4] = {
+      nf4_f16_bits(0) | nf4_f16_bits(1) << 16 | nf4_f16_bits(2) << 32 | nf4_f16_bits(3) << 48,
+      nf4_f16_bits(4) | nf4_f16_bits(5) << 16 | nf4_f16_bits(6) << 32 | nf4_f16_bits(7) << 48,
+      nf4_f16_bits(8) | nf4_f16_bits(9) << 16 | nf4_f16_bits(10) << 32 | nf4_f16_bits(11) << 48,
+      nf4_f16_bits(12) | nf4_f16_bits(13) << 16 | nf4_f16_bits(14) << 32 | nf4_f16_bits(15) << 48};
+  const uint64_t x = q < 8u ? (q < 4u ? w[0] : w[1]) : (q < 12u ? w[2] : w[3]);
+  return (uint32_t)(x >> ((q & 3u) * 16u)) & 0xffffu;
 }
 
 __device__ __forceinline__ bf16x8_t op8(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -312,10 +355,11 @@ struct AttnWave {
   bf16x8_t q[QLDS ? 1 : NQ][QLDS ? 1 : KS];
   f32x4_t o[NQ][ND];
   float m[NQ], l[NQ];
+  float sc[NQ];                                              // what a row's scores are multiplied by (base 2)
   int qpos[NQ];                                              // position of the lane's query row
 };
 
-// The NF4 byte table of common.h with 64 >> LS copies: entry b of copy c at byte
+// A table like the NF4 byte table of common.h, in fp16, with 64 >> LS copies: entry b of copy c at byte
 // (b * 64 + c) * 4 >> LS. With fewer copies a lane's address takes one more
 // instruction, and lanes of one copy meet in a bank.
 template <int LS>
@@ -328,7 +372,7 @@ __device__ __forceinline__ void fill_attn_lut(uint32_t *lut, int tid) {
 #pragma unroll
   for (int i = 0; i < (4096 >> LS) / NT; ++i) {
     const uint32_t grp = (uint32_t)tid + NT * i, b = grp >> (4 - LS);
-    const uint32_t v = nf4_bf16(b >> 4) | (nf4_bf16(b & 15u) << 16);
+    const uint32_t v = nf4_f16(b >> 4) | (nf4_f16(b & 15u) << 16);
     *reinterpret_cast<uint4 *>(lut + grp * 4) = make_uint4(v, v, v, v);
   }
 }
@@ -344,13 +388,13 @@ __device__ __forceinline__ void attn_tile(AttnWave<FMT, D, NQ> &w, const uint8_t
   const uint32_t lane4 = (uint32_t)(lane & ((64 >> LS) - 1)) << (2 + LS);
   float s[NQ][8];
   const uint8_t *sc_k = sl + T::SOFF, *sc_v = sc_k + T::SC;
-  float ksn[2], vsn[2];                                      // NF4: absmax over the operand codebook's scale
+  float ksn[2], vsn[2];                                      // NF4: absmax over the codebook's scale
   if constexpr (!MX) {
 #pragma unroll
     for (int i = 0; i < (D == 256 ? 2 : 1); ++i) {
       const int at = g * (D / 8) + (D == 64 ? c & 7 : c) + 16 * i;
-      ksn[i] = reinterpret_cast<const float *>(sc_k)[at] * kNF4InvScale;
-      vsn[i] = reinterpret_cast<const float *>(sc_v)[at] * kNF4InvScale;
+      ksn[i] = reinterpret_cast<const float *>(sc_k)[at] * kNF4HalfInv;
+      vsn[i] = reinterpret_cast<const float *>(sc_v)[at] * kNF4HalfInv;
     }
   }
   // ---- scores of positions 8g..8g+7 for the lane's query row
@@ -397,10 +441,8 @@ __device__ __forceinline__ void attn_tile(AttnWave<FMT, D, NQ> &w, const uint8_t
         bf16x8_t qv;
         if constexpr (AttnWave<FMT, D, NQ>::QLDS) qv = __builtin_bit_cast(bf16x8_t, ql[(n * KS + k) * 64 + lane]);
         else qv = w.q[n][k];
-        if constexpr (MX)
-          acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ka, qv, k == 0 ? zero : acc[n], 0, 0, 0);
-        else
-          blk[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ka, qv, (k & 1) == 0 ? zero : blk[n], 0, 0, 0);
+        if constexpr (MX) acc[n] = mfma_16x16x32<FMT>(ka, qv, k == 0 ? zero : acc[n]);
+        else blk[n] = mfma_16x16x32<FMT>(ka, qv, (k & 1) == 0 ? zero : blk[n]);
       }
       if constexpr (!MX && (k & 1)) {                        // a block of 64 is complete
         static_for<0, 4>([&](auto J) {
@@ -418,7 +460,21 @@ __device__ __forceinline__ void attn_tile(AttnWave<FMT, D, NQ> &w, const uint8_t
   });
   // ---- mask, running maximum, probabilities
   uint32_t see[NQ];
-  bf16x8_t pb[MX ? NQ : 1];
+  bf16x8_t pb[MX ? NQ : 1], pr[1];
+  // NF4: log2 of a position's largest V absmax, in the lanes of its words, less
+  // 7. Clamped so that sums of probabilities stay in float32's range.
+  float la[D == 256 ? 2 : 1];
+  if constexpr (!MX) {
+#pragma unroll
+    for (int i = 0; i < (D == 256 ? 2 : 1); ++i) {
+      float v = fabsf(vsn[i]);
+      if constexpr (D >= 128)                                // quad_perm 1,0,3,2
+        v = fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0xB1, 0xf, 0xf, true)));
+      if constexpr (D == 256)                                // quad_perm 2,3,0,1
+        v = fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x4E, 0xf, 0xf, true)));
+      la[i] = fminf(fmaxf(__builtin_amdgcn_logf(v), -60.0f), 60.0f) - 7.0f;
+    }
+  }
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
     if constexpr (MASKED) {
@@ -432,13 +488,28 @@ __device__ __forceinline__ void attn_tile(AttnWave<FMT, D, NQ> &w, const uint8_t
         s[n][j] = ok ? s[n][j] : kNegInf;
       }
     }
-    float mx = s[n][0];
+    float mx;
+    if constexpr (MX) {
+      mx = s[n][0];
 #pragma unroll
-    for (int j = 1; j < 8; ++j) mx = fmaxf(mx, s[n][j]);
-    mx = max_xor16_32(mx) * a.scale_log2;
-    // m is raised only when it has fallen 2^8 behind: until then the
-    // probabilities are up to 256 instead of 1, which costs no accuracy in
-    // float32 or bf16, and the sums need not be rescaled.
+      for (int j = 1; j < 8; ++j) mx = fmaxf(mx, s[n][j]);
+      mx = max_xor16_32(mx) * w.sc[n];
+    } else {
+      // The maximum is that of p times absmax, what enters the second product:
+      // its largest term is kept in 2^7 to 2^15, the top of fp16's range, whatever
+      // the absmax are.
+      mx = kNegInf;
+      static_for<0, 8>([&](auto J) {
+        constexpr int j = J, at = j * (D / 64);
+        s[n][j] *= w.sc[n];
+        const float y = s[n][j] + __builtin_bit_cast(float, row_bcast<at % 16>(__builtin_bit_cast(uint32_t, la[at / 16])));
+        mx = fmaxf(mx, y);
+      });
+      mx = max_xor16_32(mx);
+    }
+    // m is raised only when it has fallen 2^8 behind: until then the terms are up
+    // to 256 instead of 1, which costs no accuracy in floating point, and the
+    // sums need not be rescaled.
     if (__builtin_expect(__any(mx > w.m[n] + 8.0f), 0)) {
       mx = fmaxf(mx, w.m[n]);
       const float alpha = __builtin_amdgcn_exp2f(w.m[n] - (mx == kNegInf ? 0.0f : mx));
@@ -451,13 +522,26 @@ __device__ __forceinline__ void attn_tile(AttnWave<FMT, D, NQ> &w, const uint8_t
     float sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      s[n][j] = __builtin_amdgcn_exp2f(fmaf(s[n][j], a.scale_log2, -ms));
+      s[n][j] = __builtin_amdgcn_exp2f(MX ? fmaf(s[n][j], w.sc[n], -ms) : s[n][j] - ms);
       sum += s[n][j];
     }
     w.l[n] += sum;
-    if constexpr (MX)
-      pb[n] = op8(pk_bf16(s[n][0], s[n][1]), pk_bf16(s[n][2], s[n][3]), pk_bf16(s[n][4], s[n][5]),
-                  pk_bf16(s[n][6], s[n][7]));
+    if constexpr (MX) {
+      uint32_t h[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) h[j] = pk_bf16(s[n][2 * j], s[n][2 * j + 1]);
+      pb[n] = op8(h[0], h[1], h[2], h[3]);
+      if constexpr (NQ == 1) {
+        // what the rounding left out, as a second operand: the first product's
+        // time is its cache's, not the matrix cores'
+        uint32_t r[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          r[j] = pk_bf16(s[n][2 * j] - __builtin_bit_cast(float, h[j] << 16),
+                         s[n][2 * j + 1] - __builtin_bit_cast(float, h[j] & 0xffff0000u));
+        pr[0] = op8(r[0], r[1], r[2], r[3]);
+      }
+    }
   }
   // ---- O^T += V^T P^T
   if constexpr (MX) {
@@ -509,24 +593,28 @@ __device__ __forceinline__ void attn_tile(AttnWave<FMT, D, NQ> &w, const uint8_t
     // byte y of a lane's codes holds its values 2y and 2y+1
 #pragma unroll
     for (int y = 0; y < ND / 2; ++y) {
-      uint32_t pr[8];
+      uint32_t pv[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const uint32_t cw = vc[j][y >> 2];
-        pr[j] = (y & 3) == 0 ? fp4_pair<0>(cw, sc[j]) : (y & 3) == 1 ? fp4_pair<1>(cw, sc[j])
+        pv[j] = (y & 3) == 0 ? fp4_pair<0>(cw, sc[j]) : (y & 3) == 1 ? fp4_pair<1>(cw, sc[j])
               : (y & 3) == 2 ? fp4_pair<2>(cw, sc[j]) : fp4_pair<3>(cw, sc[j]);
       }
       uint32_t e[4], f[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        e[j] = __builtin_amdgcn_perm(pr[2 * j + 1], pr[2 * j], 0x05040100u);
-        f[j] = __builtin_amdgcn_perm(pr[2 * j + 1], pr[2 * j], 0x07060302u);
+        e[j] = __builtin_amdgcn_perm(pv[2 * j + 1], pv[2 * j], 0x05040100u);
+        f[j] = __builtin_amdgcn_perm(pv[2 * j + 1], pv[2 * j], 0x07060302u);
       }
       const bf16x8_t v0 = op8(e[0], e[1], e[2], e[3]), v1 = op8(f[0], f[1], f[2], f[3]);
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
-        w.o[n][2 * y] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v0, pb[n], w.o[n][2 * y], 0, 0, 0);
-        w.o[n][2 * y + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, pb[n], w.o[n][2 * y + 1], 0, 0, 0);
+        w.o[n][2 * y] = mfma_16x16x32<FMT>(v0, pb[n], w.o[n][2 * y]);
+        w.o[n][2 * y + 1] = mfma_16x16x32<FMT>(v1, pb[n], w.o[n][2 * y + 1]);
+        if constexpr (NQ == 1) {
+          w.o[n][2 * y] = mfma_16x16x32<FMT>(v0, pr[0], w.o[n][2 * y]);
+          w.o[n][2 * y + 1] = mfma_16x16x32<FMT>(v1, pr[0], w.o[n][2 * y + 1]);
+        }
       }
     }
   } else {
@@ -548,29 +636,59 @@ __device__ __forceinline__ void attn_tile(AttnWave<FMT, D, NQ> &w, const uint8_t
           p[j] = s[n][j] * ab[j];
           if constexpr (MASKED) p[j] = (see[n] >> j) & 1u ? p[j] : 0.0f;
         }
-        pq[n] = op8(pk_bf16(p[0], p[1]), pk_bf16(p[2], p[3]), pk_bf16(p[4], p[5]), pk_bf16(p[6], p[7]));
+        pq[n] = op8(pk_f16(p[0], p[1]), pk_f16(p[2], p[3]), pk_f16(p[4], p[5]), pk_f16(p[6], p[7]));
+      }
+      // two positions' nibbles side by side: a byte of x holds value 2y of both, of
+      // z value 2y + 1, so a table entry is the operand's pair of positions
+      uint32_t x[4], z[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t p0 = vc[2 * j], p1 = vc[2 * j + 1];
+        x[j] = (p0 & 0xf0f0u) | ((p1 >> 4) & 0x0f0fu);
+        z[j] = ((p0 << 4) & 0xf0f0u) | (p1 & 0x0f0fu);
       }
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
-        uint32_t pr[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) pr[j] = attn_lut<LS>(lut, vc[j], lane4, y);
-        uint32_t e[4], f[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          e[j] = __builtin_amdgcn_perm(pr[2 * j + 1], pr[2 * j], 0x05040100u);
-          f[j] = __builtin_amdgcn_perm(pr[2 * j + 1], pr[2 * j], 0x07060302u);
-        }
-        const bf16x8_t v0 = op8(e[0], e[1], e[2], e[3]), v1 = op8(f[0], f[1], f[2], f[3]);
+        const bf16x8_t v0 = op8(attn_lut<LS>(lut, x[0], lane4, y), attn_lut<LS>(lut, x[1], lane4, y),
+                                attn_lut<LS>(lut, x[2], lane4, y), attn_lut<LS>(lut, x[3], lane4, y));
+        const bf16x8_t v1 = op8(attn_lut<LS>(lut, z[0], lane4, y), attn_lut<LS>(lut, z[1], lane4, y),
+                                attn_lut<LS>(lut, z[2], lane4, y), attn_lut<LS>(lut, z[3], lane4, y));
         const int d = 4 * b + 2 * y;
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
-          w.o[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v0, pq[n], w.o[n][d], 0, 0, 0);
-          w.o[n][d + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, pq[n], w.o[n][d + 1], 0, 0, 0);
+          w.o[n][d] = mfma_16x16x32<FMT>(v0, pq[n], w.o[n][d]);
+          w.o[n][d + 1] = mfma_16x16x32<FMT>(v1, pq[n], w.o[n][d + 1]);
         }
       }
     });
   }
+}
+
+// A row's queries (its values lie in lanes c, c + 16, c + 32, c + 48) from bf16 to
+// fp16, divided by the power of two that brings the largest into [1, 2);
+// returns that power. Values 2^-14 and more below it lose bits that are 2^-24 of
+// the largest. A row with an infinity or a NaN keeps them.
+template <int KS>
+__device__ __forceinline__ float nf4_query(uint4 (&v)[KS]) {
+  uint32_t mag = 0;
+#pragma unroll
+  for (int i = 0; i < KS; ++i) {
+    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) mag = max(mag, max(w[j] & 0x7fffu, (w[j] >> 16) & 0x7fffu));
+  }
+  mag = __builtin_bit_cast(uint32_t, max_xor16_32(__builtin_bit_cast(float, mag << 16))) >> 16;
+  // the exponent byte, 2^-126 for what lies below; the scale of a finite row
+  const int e = min(max((int)(mag >> 7), 1), 254) - 127;
+#pragma unroll
+  for (int i = 0; i < KS; ++i) {
+    uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      w[j] = pk_f16(ldexpf(__builtin_bit_cast(float, w[j] << 16), -e), ldexpf(__builtin_bit_cast(float, w[j] & 0xffff0000u), -e));
+    v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  return ldexpf(1.0f, e);
 }
 
 // Result of one row from its unnormalised sum o (scaled by 2^-m), l and m:
@@ -616,6 +734,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? (D == 256 ? 1 : NQ == 1 ? 3 : 2)
       float red[NW * 16 * (D + 4)];                          // the waves' O tile, when they join
     };
     float sm[NW][M], sl[NW][M];
+    float qsc[M];
     uint4 q[QLDS ? NQ * KS * 64 : 1];                        // lane's operand of (tile n, step k) at (n KS + k) 64 + lane
   };
   __shared__ __attribute__((aligned(16))) Lds lds;
@@ -709,18 +828,26 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? (D == 256 ? 1 : NQ == 1 ? 3 : 2)
       w.m[n] = kNegInf;
       w.l[n] = 0.0f;
       const uint16_t *qp = a.q + (int64_t)(x.r0 + tok) * a.q_stride + (int64_t)(h * a.G + row - tok * a.G) * D;
+      w.sc[n] = a.scale_log2;
+      if (!QLDS || n % NW == wave) {                         // the waves share the loading
+        uint4 v[KS];
 #pragma unroll
-      for (int i = 0; i < KS; ++i) {
-        const int d = MX ? g * (D / 4) + i * 8 : (i >> 1) * 64 + g * 16 + (i & 1) * 8;
-        if (QLDS && (n * KS + i) % NW != wave) continue;     // the waves share the loading
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (ok) v = *reinterpret_cast<const uint4 *>(qp + d);
-        v.x ^= a.q_sign;
-        v.y ^= a.q_sign;
-        v.z ^= a.q_sign;
-        v.w ^= a.q_sign;
-        if constexpr (QLDS) lds.q[(n * KS + i) * 64 + lane] = v;
-        else w.q[n][i] = __builtin_bit_cast(bf16x8_t, v);
+        for (int i = 0; i < KS; ++i) {
+          const int d = MX ? g * (D / 4) + i * 8 : (i >> 1) * 64 + g * 16 + (i & 1) * 8;
+          v[i] = make_uint4(0, 0, 0, 0);
+          if (ok) v[i] = *reinterpret_cast<const uint4 *>(qp + d);
+          v[i].x ^= a.q_sign;
+          v[i].y ^= a.q_sign;
+          v[i].z ^= a.q_sign;
+          v[i].w ^= a.q_sign;
+        }
+        if constexpr (!MX) w.sc[n] = fminf(fmaxf(w.sc[n] * nf4_query<KS>(v), 1e-37f), 1e38f);  // not 0 or inf: masked scores are -inf, others may be 0
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+          if constexpr (QLDS) lds.q[(n * KS + i) * 64 + lane] = v[i];
+          else w.q[n][i] = __builtin_bit_cast(bf16x8_t, v[i]);
+        }
+        if constexpr (QLDS) lds.qsc[n * 16 + c] = w.sc[n];
       }
 #pragma unroll
       for (int d = 0; d < ND; ++d) w.o[n][d] = f32x4_t{0, 0, 0, 0};
@@ -729,6 +856,8 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? (D == 256 ? 1 : NQ == 1 ? 3 : 2)
     // one for the tiles under way as well.
     if constexpr (QLDS) {
       __syncthreads();
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) w.sc[n] = lds.qsc[n * 16 + c];
     } else {
 #pragma unroll
       for (int n = 0; n < NQ; ++n)

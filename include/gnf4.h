@@ -589,10 +589,14 @@ gnf4_status gnf4_kv_cache_read(const gnf4_kv_cache *cache, const gnf4_kv_batch *
  * least Hq * D), 16-byte aligned; they must not overlap. Hq % H == 0, Hq <=
  * 65536. The cache holds a row before its query attends to it, so the write
  * comes first on the stream.
- * Arithmetic: products of bf16 operands with float32 sums. MXFP4 values are
- * exact in bf16; NF4 enters as the bf16 operand codebook of the GEMMs with the
- * absmax applied in float32; probabilities are rounded to bf16 for the second
- * product. Deterministic. workspace: gnf4_kv_attention_workspace_bytes device
+ * Arithmetic: 16-bit operands, float32 sums. MXFP4 values are exact in bf16,
+ * and probabilities enter the second product as bf16 (as two bf16, the second
+ * what the first left out, when a cache head has at most 16 query rows per
+ * sequence). NF4: fp16; the codebook is rounded to fp16 at one common scale
+ * (at most 2^-11 of a value) and the absmax applied in float32, to the scores
+ * and to the probabilities, which are then rounded. For absmax of V outside
+ * 2^-60 .. 2^60 (none that a bf16 model writes) a result may be inf or 0.
+ * Deterministic. workspace: gnf4_kv_attention_workspace_bytes device
  * bytes for the same arguments, 16-byte aligned (NULL when 0), contents
  * unimportant; calls that may overlap need one each. One launch, or two when
  * the positions of a row tile are split over workgroups. */

@@ -12,12 +12,14 @@ relative to the value, the most one rounding to bf16 is off):
   r (|h| + |z| mean |h z|), and eps8 of the result.
 * weight gradients: a float32 sum whose longest chain stays below 160 terms
   (160 * 2^-24 = 1e-5) of sum |g z|.
-* attention: eps8 |out| for the result, and for the probabilities, each
-  rounded to bf16, eps8 * spread (spread = sum w |v|). NF4 operands are
-  rounded to bf16 too: eps8 * spread for the values; for the keys every
-  score moves by at most d = eps8 * reach (reach = scale * sum |q k|), which
-  changes each weight by a factor within exp(+-2 d). float32 sums, exp2
-  and the score itself: 1e-5 * (1 + reach) * spread.
+* attention: eps8 |out| for the result. MXFP4: the probabilities are each
+  rounded to bf16, eps8 * spread (spread = sum w |v|). NF4: operands in fp16
+  (eps11 = 2^-11): eps11 * spread each for the probabilities times absmax and
+  for the codebook; for the keys' codebook every score moves by at most
+  d = eps11 * reach (reach = scale * sum |q k|), which changes each weight by
+  a factor within exp(+-2 d); what lies below fp16's normal range is 2^-32 of
+  a row's largest term each. float32 sums, exp2 and the score itself:
+  1e-5 * (1 + reach) * spread.
 * lse: d (NF4) + 1e-5 * (1 + reach).
 """
 
@@ -27,6 +29,7 @@ import torch
 from oracle import attention as oa
 
 EPS8 = 2.0 ** -8
+EPS11 = 2.0 ** -11
 
 
 def to_bf16(x):
@@ -92,8 +95,8 @@ def device_cache(g, c):
 def attention_bars(fmt, out, spread, reach):
     """(bar of out, bar of lse) elementwise."""
     small = 1e-5 * (1.0 + reach)
-    d = EPS8 * reach if fmt == "nf4" else np.zeros_like(reach)
-    w = EPS8 + small + (EPS8 + np.expm1(2 * d) * (1 + EPS8) if fmt == "nf4" else 0.0)
+    d = EPS11 * reach if fmt == "nf4" else np.zeros_like(reach)
+    w = small + (2 * EPS11 + np.expm1(2 * d) * (1 + EPS8) if fmt == "nf4" else EPS8)
     return EPS8 * np.abs(out) + w[..., None] * spread * (1 + EPS8) + 1e-30, d + small
 
 
