@@ -318,3 +318,129 @@ def test_workspace_and_binding_refusals():
         g.kv_attention(q, gc, b, sinks=torch.zeros(3, device="cuda"))
     with pytest.raises(ValueError):
         g.kv_attention(q, gc, b, lse=torch.zeros(4, dtype=torch.float64, device="cuda"))
+
+
+def many(B, seed, longest=60):
+    """Lengths and new tokens of B sequences, long runs of which have no new token."""
+    r = np.random.default_rng([B, seed])
+    lens = r.integers(0, longest, B)
+    new = np.where(r.random(B) < 0.4, np.minimum(lens, r.integers(1, 4, B)), 0)
+    new[5:5 + B // 2] = 0                                    # more than 64 in a row
+    new[-1], lens[-1] = 2, longest
+    return [int(x) for x in lens], [int(x) for x in new]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("max_len", [None, 5000])
+@pytest.mark.parametrize("B", [63, 64, 65, 200])
+def test_many_sequences(fmt, max_len, B):
+    """More sequences than lanes, and more empty ones in a row; a workgroup per
+    problem (None) and shares of the positions (5000)."""
+    lens, new = many(B, 1)
+    run(fmt, Step(lens, new, 16, seed=B, max_len=max_len), 2, 2, 64, sinks=True)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G,new", [(4, 1), (16, 1), (8, 4), (10, 4)])
+def test_many_short_problems(fmt, D, G, new):
+    """So many problems that they get small workgroups, each with every row count."""
+    lens = [1 + (37 * i) % 90 for i in range(90)]
+    run(fmt, Step(lens, [min(n, new) for n in lens], 32, max_len=90), 3, G, D, window=50)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D", [64, 256])
+def test_a_wave_with_more_tiles_than_page_ids(fmt, D):
+    """One workgroup over a context of more than 64 of each wave's tiles (the
+    ids of a wave's next 64 pages are held in its lanes)."""
+    n = 64 * 256 + 300
+    run(fmt, Step([n, 40], [2, 1], 16, max_len=1000), 1, 1, D)
+    run(fmt, Step([n], [1], 64, max_len=1000), 1, 1, D, window=n - 150)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("lens", [[700], [3000, 40]])
+def test_values_of_very_different_size(fmt, D, lens):
+    """Values 2^-20 to 2^20 apart between positions, blocks 2^-6 to 2^6, and positions that are zero."""
+    step = Step(lens, [2] * len(lens), 16)
+    r = np.random.default_rng([D, len(lens)])
+    c = oa.Cache(fmt, step.n_pages, 16, 2, D)
+    whole = step.whole()
+    k, v = r.standard_normal((2, whole.T, 2, D))
+    e = r.integers(-20, 21, (whole.T, 2, 1)) + np.repeat(r.integers(-6, 7, (whole.T, 2, D // 64)), 64, -1)
+    v = v * np.exp2(e) * (r.random((whole.T, 2, 1)) < 0.8)
+    c.write(whole.oracle(), 2.0 * k, v)
+    run(fmt, step, 2, 4, D, cache=c)
+    c.write(whole.oracle(), k, v * 2.0 ** -30)
+    run(fmt, step, 2, 4, D, cache=c, sinks=True)
+    c.write(whole.oracle(), k, np.zeros_like(v))
+    _, out = run(fmt, step, 2, 4, D, cache=c)
+    assert not out.any()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("size", [-100, -30, 30, 60])
+def test_queries_of_every_size(fmt, size):
+    """Query rows far from 1, undone by the scale or by the keys' size."""
+    step = Step([200, 60], [3, 1], 16)
+    c = filled(fmt, step, 2, 64, 2)
+    _, q = queries(step.T, 8, 64, 3)
+    q = q * 2.0 ** (size + np.arange(8) % 3)[:, None]
+    run(fmt, step, 2, 4, 64, cache=c, q=to_bf16(q), scale=0.125 * 2.0 ** -size)
+
+
+def test_positions_behind_four_gib():
+    """A sequence whose pages are the first and the last of a cache longer than 2^32 bytes."""
+    g = gnf4()
+    page, H, D = 65536, 4, 256
+    n = (1 << 32) // (page * H * D // 2) + 2
+    say("kv_attention large cache", n, "pages")
+    gc = g.empty_kv_cache("mxfp4", n, page, H, D)
+    r = np.random.default_rng(3)
+    near = Step([70], [70], 16, spare=0)
+    k, v = r.standard_normal((2, 70, H, D))
+    small = oa.Cache("mxfp4", near.n_pages, 16, H, D)
+    small.write(near.oracle(), k, v)
+    far = Step([70], [2], 64)
+    far.page, far.n_pages, far.pages = page, n, np.array([[n - 1]])
+    b = far.device(g)
+    rows = g.KVBatch(dev(np.array([0, 70], dtype=np.int32)), b.lens, b.pages, 70, 70, 70)
+    g.kv_cache_write(gc, dev(k.astype(np.float32)).bfloat16(), dev(v.astype(np.float32)).bfloat16(), rows)
+    small.write(near.oracle(), *(to_bf16(x)[1] for x in (k, v)))
+    near.new, near.offsets, near.T = [2], [0, 2], 2
+    bits, q = queries(2, 8, D, 4)
+    out = g.kv_attention(dev_bf16(bits), gc, b)
+    check_attention("mxfp4", values(out), None, oa.attend(q, small, near.oracle(), D ** -0.5))
+
+
+def test_two_streams_and_graphs_with_their_own_workspaces():
+    """Two captured calls and two eager ones at once, a workspace each."""
+    g = gnf4()
+    say("kv_attention two graphs")
+    steps = [Step([3000, 1200], [1, 1], 64, seed=1), Step([2500], [3], 32, seed=2)]
+    gcs = [device_cache(g, filled("nf4", s, 2, 128, 3)) for s in steps]
+    bs = [s.device(g) for s in steps]
+    qs = [dev_bf16(queries(s.T, 8, 128, 5)[0]) for s in steps]
+    want = [g.kv_attention(*a) for a in zip(qs, gcs, bs)]
+    outs = [torch.zeros_like(w) for w in want]
+    graphs = []
+    for q, c, b, o in zip(qs, gcs, bs, outs):
+        ws = torch.empty(g.kv_attention_workspace_bytes(c, b, 8), dtype=torch.uint8, device="cuda")
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            g.kv_attention(q, c, b, out=o, workspace=ws)
+        graphs.append((gr, ws))
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for i in range(4):
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        for s, (gr, _) in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                gr.replay()
+        eager = [g.kv_attention(*a) for a in zip(qs, gcs, bs)]
+        torch.cuda.synchronize()
+        for w, o, e in zip(want, outs, eager):
+            assert torch.equal(w, o) and torch.equal(w, e), i

@@ -250,3 +250,21 @@ def test_binding_refusals():
     with pytest.raises(g.Gnf4Error) as e:
         g.kv_cache_write(gc, x, x, g.KVBatch(b.offsets, b.lens, b.pages, 5, 0, 5))
     assert e.value.status == 1
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("B", [63, 65, 200])
+def test_many_sequences(fmt, B):
+    """More sequences than lanes, and more without new tokens in a row."""
+    r = np.random.default_rng(B)
+    lens = r.integers(0, 40, B)
+    new = np.where(r.random(B) < 0.5, lens, np.minimum(lens, 1))
+    new[3:3 + B // 2] = 0
+    new[-1] = lens[-1] = 33
+    step = Step([int(x) for x in lens], [int(x) for x in new], 16, seed=B)
+    k, kd, v, vd = rows_of(step.T, 2, 64, 4)
+    c, gc = run_write(fmt, step, 2, 64, k, v, kd, vd)
+    g = gnf4()
+    want = c.read(step.oracle(), *(np.full((step.T, 2, 64), 7.0, np.float32) for _ in range(2)))
+    for w, got in zip(want, g.kv_cache_read(gc, step.device(g), torch.float32)):
+        assert np.array_equal(w, got.cpu().numpy())
