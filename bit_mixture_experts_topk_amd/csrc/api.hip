@@ -792,7 +792,7 @@ static gnf4_status check_kv_sizes(const gnf4_kv_cache *c, const gnf4_kv_batch *b
   if (b->max_pages < 1 || (int64_t)b->max_pages * c->page_size > (int64_t)1 << 30)
     return fail(GNF4_ERR_INVALID_ARG, "max_pages = %d must be positive, max_pages * page_size at most 2^30",
                 b->max_pages);
-  if ((int64_t)b->n_tokens * c->H * (c->D / 4) > 0x7fffffffLL * 256)
+  if (b->n_tokens > 1 << 27 || (int64_t)b->n_tokens * c->H * (c->D / 4) > 0x7fffffffLL * 256)
     return fail(GNF4_ERR_UNSUPPORTED, "too many rows for one call");
   return ok();
 }

@@ -797,9 +797,10 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? (D == 256 ? 1 : NQ == 1 ? 3 : 2)
     mt = (mt & 1) ? x.mts - 1 - (mt >> 1) : mt >> 1;
     const int row0 = mt * M, last = min(row0 + M, x.rows) - 1;
     const int full_hi = x.start + row0 / a.G;                // every row sees from full_lo to full_hi
-    const int full_lo = a.window > 0 ? x.start + last / a.G - a.window + 1 : 0;
+    // (not below 0 - window: a window may be as wide as the type)
+    const int full_lo = a.window > 0 ? max(x.start + last / a.G, 0) - a.window + 1 : 0;
     // the run's positions, among those that some row of this tile sees
-    const int lo = a.window > 0 ? max(0, full_hi - a.window + 1) & ~31 : 0;
+    const int lo = a.window > 0 ? max(0, max(full_hi, 0) - a.window + 1) & ~31 : 0;
     const int hi = min(x.hi, x.start + last / a.G + 1);
     const int t0 = lo + q0 * kAttnUnit, t1 = q1 == x.units ? hi : min(hi, lo + q1 * kAttnUnit);
 
@@ -824,7 +825,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? (D == 256 ? 1 : NQ == 1 ? 3 : 2)
     for (int n = 0; n < NQ; ++n) {
       const int row = row0 + n * 16 + c, tok = row / a.G;
       const bool ok = row < x.rows;
-      w.qpos[n] = ok ? x.start + tok : -1;
+      w.qpos[n] = ok ? max(x.start + tok, -1) : -1;             // below 0: sees nothing
       w.m[n] = kNegInf;
       w.l[n] = 0.0f;
       const uint16_t *qp = a.q + (int64_t)(x.r0 + tok) * a.q_stride + (int64_t)(h * a.G + row - tok * a.G) * D;
@@ -1071,12 +1072,12 @@ bool kv_attention_plan(int32_t format, int32_t D, int32_t H, int32_t G, int32_t 
   int64_t len = std::max<int64_t>(max_len, 1);
   p->tile_tokens = (int32_t)std::min<int64_t>((M - 1 + G - 1) / G + 1, max_new);
   if (window > 0) len = std::min<int64_t>(len, (int64_t)window + p->tile_tokens - 1 + 31);
-  if (p->items > 0x7fffffffLL) return false;
+  if (p->items >= 1 << 23) return false;                     // a launch has fewer than 2^32 threads
   p->n_mt = (int32_t)n_mt;
   p->shared = len > kAttnShort;
   p->small = !p->shared && p->items >= kAttnGroups;
   // the runs are counted in 32 bits
-  if (p->shared && p->items * ((capacity + kAttnUnit - 1) / kAttnUnit) > 0x7fffffffLL) p->shared = 0;
+  if (p->shared && p->items * ((capacity + kAttnUnit - 1) / kAttnUnit) > 0x7fff0000LL) p->shared = 0;
   p->bytes = p->shared ? (size_t)(2 * kAttnGroups * M) * (D + 2) * 4 : 0;
   return true;
 }

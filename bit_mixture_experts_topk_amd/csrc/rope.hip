@@ -291,7 +291,23 @@ __global__ __launch_bounds__(16 * kDwSlices) void norm_rope_dw_kernel(const floa
 
 int32_t rope_dx_blocks(int32_t T) { return std::min<int32_t>(T, 1024); }
 
-hipError_t launch_norm_rope(const RopeArgs &a, hipStream_t s) {
+// A launch has fewer than 2^32 threads: more tokens than this in several.
+constexpr int kRopeTokens = 1 << 23;
+
+hipError_t launch_norm_rope(const RopeArgs &args, hipStream_t s) {
+  if (args.T > kRopeTokens) {
+    RopeArgs a = args;
+    for (int64_t t = 0; t < args.T; t += kRopeTokens) {
+      a.T = (int32_t)std::min<int64_t>(args.T - t, kRopeTokens);
+      if (args.Hq) a.q = args.q + t * args.q_stride, a.q_out = args.q_out + t * args.q_out_stride;
+      if (args.Hk) a.k = args.k + t * args.k_stride, a.k_out = args.k_out + t * args.k_out_stride;
+      if (args.positions) a.positions = args.positions + t;
+      const hipError_t e = launch_norm_rope(a, s);
+      if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+  }
+  const RopeArgs &a = args;
   const int rows = a.Hq + a.Hk;
   const int lpr = a.D <= 64 ? 8 : a.D <= 128 ? 16 : 32, rpi = kRopeThreads / lpr;
   // few tokens: one round of head rows per workgroup; many: all of a token's

@@ -477,7 +477,8 @@ typedef struct {
  * with them: row r stands at position lens[b] - offsets[b+1] + r. Position p of
  * sequence b lies on page pages[b * max_pages + p / page_size], place p %
  * page_size. offsets int32 [B+1] ascending, lens int32 [B], pages int32
- * [B][max_pages], all on the device; max_pages * page_size <= 2^30; B <= 2^20.
+ * [B][max_pages], all on the device; max_pages * page_size <= 2^30; B <= 2^20;
+ * n_tokens <= 2^27.
  * max_new (>= 1) is a bound on the new tokens of any one sequence: attention
  * does not compute rows past it. max_len is the longest length expected: it
  * decides how the work is split, and longer sequences are still computed
@@ -587,7 +588,8 @@ gnf4_status gnf4_kv_cache_read(const gnf4_kv_cache *cache, const gnf4_kv_batch *
  * parts of a context can be joined.
  * q, out: bf16 bits [n_tokens][Hq][D] with token strides (multiples of 8, at
  * least Hq * D), 16-byte aligned; they must not overlap. Hq % H == 0, Hq <=
- * 65536. The cache holds a row before its query attends to it, so the write
+ * 65536; UNSUPPORTED when B * H * ceil(max_new * Hq / (16 H)) is 2^23 or more
+ * and larger row tiles do not bring it below. The cache holds a row before its query attends to it, so the write
  * comes first on the stream.
  * Arithmetic: 16-bit operands, float32 sums. MXFP4 values are exact in bf16,
  * and probabilities enter the second product as bf16 (as two bf16, the second

@@ -200,3 +200,14 @@ def test_workspace_does_not_grow_with_the_bounds(L):
                 assert need <= 256 << 20, (D, max_len, n, new, need)
                 if max_len <= 128:
                     assert need == 0
+
+
+def test_launches_stay_below_their_thread_limit(L):
+    """Problems and tokens whose launch would have 2^32 threads are refused."""
+    ok = dict(B=1 << 19, H=8, n=1 << 19, max_new=1, max_len=100)
+    for kw, bad in ((ok, False), (dict(ok, B=1 << 20, n=1 << 20), True), (dict(ok, max_new=1 << 19), True)):
+        c, b = (ctypes.byref(x) for x in structs(kw))
+        st = L.gnf4_kv_attention(None, 1024, c, b, 8, 0.1, 0, None, A, 1024, None, None, 0, None)
+        refused(st, UNSUPPORTED if bad else INVALID, "too many rows" if bad else "q")
+    c, b = (ctypes.byref(x) for x in structs(dict(n=(1 << 27) + 1)))
+    refused(L.gnf4_kv_cache_write(c, b, A, 256, A, 256, None), UNSUPPORTED, "too many rows")

@@ -444,3 +444,14 @@ def test_two_streams_and_graphs_with_their_own_workspaces():
         torch.cuda.synchronize()
         for w, o, e in zip(want, outs, eager):
             assert torch.equal(w, o) and torch.equal(w, e), i
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("window", [3, 2 ** 31 - 1])
+def test_windows_of_rows_below_position_zero(fmt, window):
+    """A tile whose first rows stand below position 0: the widest window takes nothing from its other rows."""
+    step = Step([9, 40], [9, 3], 16)
+    c = filled(fmt, step, 1, 64, 8)
+    step.lens[0] = 4                                         # rows at -5 .. 3
+    _, out = run(fmt, step, 1, 2, 64, window=window, cache=c)
+    assert not out[:5].any() and out[5:].any(-1).any(-1).all()

@@ -217,3 +217,19 @@ def test_binding_refusals():
         g.qk_norm_rope(c["qd"], c["kd"], c["posd"], rope, wq=c["wd"][0][:64])
     with pytest.raises(ValueError):
         g.qk_norm_rope(c["qd"].cpu(), c["kd"], c["posd"], rope)
+
+
+def test_more_tokens_than_a_launch_has_threads_for():
+    """2^24 tokens and some: every one as in a call of its own part."""
+    g = gnf4()
+    T = (1 << 24) + 5
+    say("norm_rope", T, "tokens")
+    q = torch.randn((T, 1, 16), dtype=torch.bfloat16, device="cuda")
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    w = torch.ones(16, dtype=torch.bfloat16, device="cuda")
+    rope = g.rope_frequencies(16, 10000.0)
+    k = torch.empty((T, 0, 16), dtype=torch.bfloat16, device="cuda")
+    out = g.qk_norm_rope(q, k, pos, rope, w, None)[0]
+    for lo, hi in ((0, 9), ((1 << 23) - 4, (1 << 23) + 4), ((1 << 24) - 4, T)):
+        part = g.qk_norm_rope(q[lo:hi].contiguous(), k[lo:hi], pos[lo:hi].contiguous(), rope, w, None)[0]
+        assert torch.equal(out[lo:hi], part)
