@@ -351,7 +351,7 @@ __device__ __forceinline__ void static_for(F &&f) {
 template <int FMT, int D, int NQ>
 struct AttnWave {
   static constexpr int KS = D / 32, ND = D / 16;
-  static constexpr bool QLDS = NQ > 2;                       // more tiles: their queries stay in LDS
+  static constexpr bool QLDS = NQ > 2 || (D == 256 && NQ > 1);  // many results: the queries stay in LDS
   bf16x8_t q[QLDS ? 1 : NQ][QLDS ? 1 : KS];
   f32x4_t o[NQ][ND];
   float m[NQ], l[NQ];
@@ -1044,14 +1044,14 @@ __global__ __launch_bounds__(kJoinThreads) void kv_attn_join_kernel(KvAttnArgs a
 template <int FMT, int D, int NQ>
 struct AttnCfg {
   static constexpr bool MX = FMT == GNF4_MXFP4;
-  static constexpr int NW = D == 256 && !MX ? 4 : 8;
+  static constexpr int NW = D == 256 && (!MX || NQ == 2) ? 4 : 8;
   static constexpr int S = NW == 8 && MX && D <= 128 ? 3 : 2;
 };
 
 // The most 16-row tiles of a wave whose results the registers hold: a step
 // decodes K and V once for all of them.
 constexpr int attn_most_tiles(int format, int D) {
-  return D == 256 ? 1 : D == 64 ? 4 : format == GNF4_MXFP4 ? 3 : 2;
+  return D == 256 ? 2 : D == 64 ? 4 : format == GNF4_MXFP4 ? 3 : 2;
 }
 
 constexpr int kAttnShort = 1024;
@@ -1062,10 +1062,17 @@ constexpr int kAttnShort = 1024;
 bool kv_attention_plan(int32_t format, int32_t D, int32_t H, int32_t G, int32_t B, int64_t n_tokens, int32_t max_new,
                        int64_t max_len, int64_t capacity, int32_t window, KvAttnPlan *p) {
   const int64_t rows = (int64_t)max_new * G;
-  p->nq = rows <= 16 || D == 256 ? 1 : rows <= 32 ? 2 : attn_most_tiles(format, D);
+  p->nq = rows <= 16 ? 1 : rows <= 32 ? 2 : attn_most_tiles(format, D);
   // a short context is a small problem also with many rows
   const int64_t seen = window > 0 ? std::min<int64_t>(max_len, (int64_t)window + 64) : max_len;
   if (seen <= kAttnShort && p->nq > 2) p->nq = 2;
+  // Two tiles of 256 values take four waves a compute unit. NF4 has no more with
+  // one (2 x 1024 rows of 4 heads over 4000: 401 us, 565 with one); MXFP4 has
+  // eight, so that two pay only over many positions (226 us, 262; 8 x 40 rows
+  // over 4097: 39 us, 34).
+  if (D == 256 && format == GNF4_MXFP4 && p->nq == 2 &&
+      (seen <= kAttnShort || (int64_t)B * H * ((rows + 31) / 32) * seen < 1 << 19))
+    p->nq = 1;
   const int M = 16 * p->nq;
   const int64_t n_mt = (rows + M - 1) / M;
   p->items = (int64_t)B * n_mt * H;
@@ -1098,6 +1105,9 @@ static hipError_t attn_nq(const KvAttnArgs &a, const KvAttnPlan &p, hipStream_t 
     if (p.small && p.nq == 2) return attn_go<FMT, D, 2, 4, 2>(a, p, s);
     constexpr int most = attn_most_tiles(FMT, D);
     if (p.nq == most && most > 2) return attn_go<FMT, D, most, AttnCfg<FMT, D, most>::NW, AttnCfg<FMT, D, most>::S>(a, p, s);
+    if (p.nq == 2) return attn_go<FMT, D, 2, AttnCfg<FMT, D, 2>::NW, AttnCfg<FMT, D, 2>::S>(a, p, s);
+  }
+  if constexpr (D == 256) {
     if (p.nq == 2) return attn_go<FMT, D, 2, AttnCfg<FMT, D, 2>::NW, AttnCfg<FMT, D, 2>::S>(a, p, s);
   }
   if (p.small) return attn_go<FMT, D, 1, 4, 2>(a, p, s);

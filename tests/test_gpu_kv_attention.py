@@ -455,3 +455,12 @@ def test_windows_of_rows_below_position_zero(fmt, window):
     step.lens[0] = 4                                         # rows at -5 .. 3
     _, out = run(fmt, step, 1, 2, 64, window=window, cache=c)
     assert not out[:5].any() and out[5:].any(-1).any(-1).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_wide_heads_in_pairs_of_tiles(fmt):
+    """D = 256 with more than 16 rows over many positions: two tiles per wave, of
+    which the last is part empty."""
+    run(fmt, Step([2100, 1300], [50, 33], 32), 2, 8, 256, window=0, sinks=True)
+    run(fmt, Step([1500] * 2, [20, 1], 64), 1, 1, 256, window=1100)
+    run(fmt, Step([2000] * 24, [5] * 24, 64), 2, 4, 256)
