@@ -6,5 +6,6 @@ include/gnf4.h); ``gnf4`` is its Python binding. Build with
 """
 
 from . import gnf4  # noqa: F401
-from .gnf4 import (MXFP4, NF4, NF4_DQ, PackedWeights, build_id, combine, dequant,  # noqa: F401
-                   grouped_gemm, quantize, route)
+from .gnf4 import (KVBatch, KVCache, MXFP4, NF4, NF4_DQ, PackedWeights, Rope, build_id, combine,  # noqa: F401
+                   dequant, empty_kv_cache, grouped_gemm, kv_attention, kv_cache_read, kv_cache_write,
+                   qk_norm_rope, qk_norm_rope_dx, quantize, rope_frequencies, route)

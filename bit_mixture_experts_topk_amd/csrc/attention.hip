@@ -20,10 +20,21 @@
 // the next. A problem that lies in several shares is put together by a second
 // kernel.
 //
-// Bound by the cache's bytes: a wave keeps its next tiles in flight straight
-// into LDS (global_load_lds, no registers), S slots of its own, so that a
-// compute unit has about 70 KB under way and its registers hold four waves per
-// SIMD, which cover each other's latencies.
+// With few rows it is bound by the cache's bytes: a wave keeps its next tiles in
+// flight straight into LDS (global_load_lds, no registers), S slots of its own,
+// so that a compute unit has about 70 KB under way, and two waves per SIMD take
+// turns at decoding and multiplying. MXFP4, 16 sequences of 16 to 32 thousand
+// positions of 8 heads of 128: 443 MB in 85 us, 5.2 TB/s (a plain read of
+// 1 GiB: 5.5), and 5 us to join. With less to read per workgroup its ends
+// show: NF4, 32 sequences of 0.8 to 8 thousand positions of 4 heads, 86 MB in
+// 34 us, of which a workgroup spends 20 in its tiles (at 5.6 TB/s) and the
+// rest in finding its share, in the first pages, queries and tiles of each of
+// its problems, and in joining its waves.
+// With many rows it is bound by instructions: 2 x 1024 tokens of 32 heads over
+// up to 8192 positions, MXFP4: 260 us, 715 TFLOP/s (a large bf16 product of the
+// library: 1137). Vector instructions (exponentials, roundings, decoding) take
+// about 55 % of a SIMD's cycles and the products 29 %; its two waves overlap
+// them in part.
 //
 // No transposes. v_mfma_f32_16x16x32 (bf16 or f16) takes A rows from lanes 0..15 with 8
 // consecutive k per lane group g = lane / 16, and leaves C with its column in
@@ -359,9 +370,9 @@ struct AttnWave {
   int qpos[NQ];                                              // position of the lane's query row
 };
 
-// A table like the NF4 byte table of common.h, in fp16, with 64 >> LS copies: entry b of copy c at byte
-// (b * 64 + c) * 4 >> LS. With fewer copies a lane's address takes one more
-// instruction, and lanes of one copy meet in a bank.
+// A table like the NF4 byte table of common.h, in fp16, with 64 >> LS copies:
+// entry b of copy c at byte (b * 64 + c) * 4 >> LS. With fewer copies a lane's
+// address takes one more instruction, and lanes of one copy meet in a bank.
 template <int LS>
 __device__ __forceinline__ uint32_t attn_lut(const uint32_t *lut, uint32_t w, uint32_t lane4, int byte) {
   return lut_read(lut, lut_addr(w, lane4, byte) >> LS);
@@ -842,7 +853,8 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? (D == 256 ? 1 : NQ == 1 ? 3 : 2)
           v[i].z ^= a.q_sign;
           v[i].w ^= a.q_sign;
         }
-        if constexpr (!MX) w.sc[n] = fminf(fmaxf(w.sc[n] * nf4_query<KS>(v), 1e-37f), 1e38f);  // not 0 or inf: masked scores are -inf, others may be 0
+        if constexpr (!MX)                                   // not 0 or inf: masked scores are -inf, others may be 0
+          w.sc[n] = fminf(fmaxf(w.sc[n] * nf4_query<KS>(v), 1e-37f), 1e38f);
 #pragma unroll
         for (int i = 0; i < KS; ++i) {
           if constexpr (QLDS) lds.q[(n * KS + i) * 64 + lane] = v[i];
@@ -1038,9 +1050,11 @@ __global__ __launch_bounds__(kJoinThreads) void kv_attn_join_kernel(KvAttnArgs a
   }
 }
 
-// Waves and slots of a workgroup that has a compute unit to itself, by what the
-// registers (four waves per SIMD have 128 each, two 256) and the LDS (160 KB,
-// 64 of them the NF4 table) hold.
+// Waves and slots of a workgroup that has a compute unit to itself: eight waves
+// of up to 256 registers, four where a wave of 256 values has two tiles or the
+// slots would not fit beside the NF4 table (64 of 160 KB); the third slot where
+// there is room (for NF4 it takes a smaller table, which costs more than the
+// slot gains: 39 us became 42 in the 32 sequences above).
 template <int FMT, int D, int NQ>
 struct AttnCfg {
   static constexpr bool MX = FMT == GNF4_MXFP4;

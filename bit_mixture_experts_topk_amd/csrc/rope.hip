@@ -14,7 +14,11 @@
 // float32 operations. A head row lies in 8, 16 or 32 lanes (8 values each, one
 // 16-byte access), its sums in DPP steps; a workgroup takes one token at a
 // time, so that the angles, formed in float64 (pos * f of far positions has
-// no fraction left in float32), are computed once for all its heads.
+// no fraction left in float32), are computed once for all its heads. 8192
+// tokens of 64 + 4 heads of 128: 57 us, 5.0 TB/s (a 1 GiB copy: 5.2); backward,
+// 4096 tokens of 32 + 4 heads: 32.5 us, 3.5 TB/s, and 4 for the weights' sums.
+// The backward has three streams and two chained row sums per row, and its
+// workgroups keep the weights' sums in registers over all their tokens.
 #include <algorithm>
 
 #include "rope.h"

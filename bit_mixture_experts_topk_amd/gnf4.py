@@ -6,7 +6,8 @@ device pointers and torch's current HIP stream, and raises on a non-OK status.
 There is no fallback: if the library is missing or a call fails, it raises.
 
 Names follow the C ABI in include/gnf4.h: route, grouped_gemm, combine,
-dequant, quantize, nf4_codebook, last_error, build_id.
+dequant, quantize, nf4_codebook, rope_frequencies, qk_norm_rope, kv_cache_write,
+kv_cache_read, kv_attention, last_error, build_id.
 """
 
 import ctypes
