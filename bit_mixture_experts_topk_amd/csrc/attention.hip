@@ -887,8 +887,6 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? (D == 256 ? 1 : NQ == 1 ? 3 : 2)
         bad &= ~(3u << (2 * next));
         bad |= attn_send<FMT, D>(pl, ahead & 63, first + ahead * ROUND, ring_at + next * T::BYTES, lane) << (2 * next);
         wait_vm<(S - 1) * T::LOADS>();
-      } else if (S > 3 && i + 2 < tiles) {
-        wait_vm<2 * T::LOADS>();
       } else if (S > 2 && i + 1 < tiles) {
         wait_vm<T::LOADS>();
       } else {
@@ -1135,9 +1133,9 @@ hipError_t launch_kv_attention(const KvAttnArgs &args, const KvAttnPlan &p, int3
   a.tile_tokens = p.tile_tokens;
   // The running maximum is taken before the scale, which therefore must not be
   // negative (the queries change sign instead) nor 0 (0 times the -inf of a
-  // masked place; 2^-100 leaves the weights equal).
+  // masked place; 2^-100 leaves the weights equal) nor infinite (0 times that).
   a.q_sign = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
-  a.scale_log2 = std::max(std::fabs(a.scale_log2), 0x1p-100f);
+  a.scale_log2 = std::min(std::max(std::fabs(a.scale_log2), 0x1p-100f), 0x1p127f);
   if (format == GNF4_MXFP4) {
     if (a.kv.D == 64) return attn_nq<GNF4_MXFP4, 64>(a, p, s);
     if (a.kv.D == 128) return attn_nq<GNF4_MXFP4, 128>(a, p, s);
