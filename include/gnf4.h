@@ -598,6 +598,8 @@ gnf4_status gnf4_kv_cache_read(const gnf4_kv_cache *cache, const gnf4_kv_batch *
  * (at most 2^-11 of a value) and the absmax applied in float32, to the scores
  * and to the probabilities, which are then rounded. For absmax of V outside
  * 2^-60 .. 2^60 (none that a bf16 model writes) a result may be inf or 0.
+ * Terms below 2^-31 of a row's largest vanish (also those of a block of 64
+ * values beside a block of the same head that is so much larger).
  * Deterministic. workspace: gnf4_kv_attention_workspace_bytes device
  * bytes for the same arguments, 16-byte aligned (NULL when 0), contents
  * unimportant; calls that may overlap need one each. One launch, or two when

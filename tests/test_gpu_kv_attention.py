@@ -464,3 +464,19 @@ def test_wide_heads_in_pairs_of_tiles(fmt):
     run(fmt, Step([2100, 1300], [50, 33], 32), 2, 8, 256, window=0, sinks=True)
     run(fmt, Step([1500] * 2, [20, 1], 64), 1, 1, 256, window=1100)
     run(fmt, Step([2000] * 24, [5] * 24, 64), 2, 4, 256)
+
+
+@pytest.mark.parametrize("D", [128, 256])
+def test_blocks_of_a_head_far_apart(D):
+    """One block of V 2^-18 of the others: the products of its probabilities reach
+    below fp16's normal range, 2^-25 of absolute error beside terms around 2^-13,
+    which is 2^-12 of their sum and stays inside the bar's two 2^-11."""
+    step = Step([400, 60], [2, 1], 16)
+    r = np.random.default_rng(D)
+    c = oa.Cache("nf4", step.n_pages, 16, 2, D)
+    whole = step.whole()
+    k, v = r.standard_normal((2, whole.T, 2, D))
+    v[..., 64:128] *= 2.0 ** -18
+    c.write(whole.oracle(), k, v)
+    _, out = run("nf4", step, 2, 4, D, cache=c)
+    assert (out[..., 64:128] != 0).float().mean() > 0.99
